@@ -137,7 +137,8 @@ def _pages(case, gen):
 
 def _codes(x):
     """int8 codes and the scale of each last-dimension vector of fp32 values."""
-    s = x.abs().amax(-1, keepdim=True) / 127.0
+    top = x.abs().amax(-1, keepdim=True)
+    s = top / torch.full_like(top, 127.0)  # by a number it would be a product with the reciprocal
     c = torch.where(s > 0, torch.round(x / s), torch.zeros_like(x))
     return c, s.squeeze(-1)
 
