@@ -12,6 +12,7 @@ from ._binding import (  # noqa: F401
     QSA_ERR_WORKSPACE,
     QSA_ERRBIT_SLOT_RANGE,
     QSA_ERRBIT_Q_RANGE,
+    QSA_ERRBIT_TIMEOUT,
     QSA_ERRBIT_WIDTH_RANGE,
     QSA_MAX_BLOCK,
     QSA_MAX_SLOTS_PER_SPLIT,
@@ -47,6 +48,14 @@ from .context_parallel import (  # noqa: F401
     shard_ranges,
     sparse_prefill_context_parallel,
 )
+from .layer import (  # noqa: F401
+    pack_index_keys,
+    paged_decode,
+    qk_norm_rope,
+    qsa_paged_decode_plan,
+    qsa_select_slots_workspace_bytes,
+    select_slots,
+)
 
 __all__ = [
     "sparse_prefill", "sparse_prefill_from_host", "qsa_sparse_prefill", "qsa_sparse_prefill_noalloc",
@@ -56,4 +65,6 @@ __all__ = [
     "qsa_combine_peer_records", "combine_peer_records", "PeerExchange", "release_peer_exchanges",
     "qsa_sparse_prefill_plan", "qsa_sparse_prefill_workspace_bytes", "qsa_status_string", "qsa_last_error_detail", "qsa_abi_version",
     "load_library", "QSAError", "qsa_probe_gather", "qsa_probe_mma_operands",
+    "qk_norm_rope", "pack_index_keys", "select_slots", "paged_decode", "qsa_select_slots_workspace_bytes",
+    "qsa_paged_decode_plan",
 ]

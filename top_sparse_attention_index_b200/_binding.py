@@ -22,6 +22,7 @@ QSA_ERR_CUDA = 4
 QSA_ERRBIT_SLOT_RANGE = 0x1
 QSA_ERRBIT_WIDTH_RANGE = 0x2
 QSA_ERRBIT_Q_RANGE = 0x4
+QSA_ERRBIT_TIMEOUT = 0x10
 QSA_MAX_SLOTS_PER_SPLIT = 2240
 QSA_MAX_BLOCK = 16
 QSA_STATIC_SCRATCH_BYTES = 16 << 20
@@ -64,6 +65,21 @@ SIGNATURES = {
     "qsa_ipc_export": (_i32, [_p, _p, ctypes.POINTER(ctypes.c_uint64)]),
     "qsa_ipc_import": (_i32, [_p, ctypes.POINTER(_p)]),
     "qsa_ipc_close": (_i32, [_p]),
+    # include/qsa_layer.h
+    "qsa_qk_norm_rope": (_i32, [_p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _p, _p, _f, _f, _p,
+                                _i64, _p, _i32, _i32, ctypes.POINTER(_i32), _i32, _f, _i32, _i32,
+                                _i32, _i32, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _p,
+                                _i64, _i32, _f, _f, _p, _p]),
+    "qsa_pack_index_keys": (_i32, [_p, _i64, _p, _i32, _i32, _i32, _i64, _p, _i64, _p, _p, _p]),
+    "qsa_select_slots_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32]),
+    "qsa_select_slots": (_i32, [_p, _i64, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _p, _p, _i32,
+                                _i32, _i32, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _p,
+                                _i64, _p, _p, _sz, _p, _p]),
+    "qsa_paged_decode_plan": (_i32, [_i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                                     ctypes.POINTER(_sz)]),
+    "qsa_paged_decode": (_i32, [_p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _p, _i32,
+                                _i32, _i32, _i32, _i32, _i64, _i32, _f, _i32, _f, _f, _p, _i64,
+                                _i64, _p, _i32, _p, _sz, _p, _p]),
     "qsa_status_string": (ctypes.c_char_p, [_i32]),
     "qsa_last_error_detail": (ctypes.c_char_p, []),
 }

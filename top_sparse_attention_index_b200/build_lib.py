@@ -19,8 +19,10 @@ CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 LIBRARY = PKG / "libqsa.so"
 SOURCES = [CSRC / "qsa_api.cu", CSRC / "qsa_attn.cu", CSRC / "qsa_noalloc.cu", CSRC / "qsa_probe.cu",
-           CSRC / "qsa_probe_mma.cu", CSRC / "qsa_peer.cu"]
-DEPENDS = SOURCES + [CSRC / "qsa_internal.h", CSRC / "qsa_ptx.cuh", INCLUDE / "qsa.h",
+           CSRC / "qsa_probe_mma.cu", CSRC / "qsa_peer.cu",
+           CSRC / "qsa_rope.cu", CSRC / "qsa_select.cu", CSRC / "qsa_decode.cu"]
+DEPENDS = SOURCES + [CSRC / "qsa_layer.cuh", INCLUDE / "qsa_layer.h",
+                     CSRC / "qsa_internal.h", CSRC / "qsa_ptx.cuh", INCLUDE / "qsa.h",
                      INCLUDE / "qsa_probe.h", INCLUDE / "qsa_peer.h"]
 
 NVCC_FLAGS = [

@@ -1,0 +1,85 @@
+// qsa_layer.cuh -- shared by the layer operators (qsa_rope.cu, qsa_select.cu,
+// qsa_decode.cu): host-side argument helpers and small device functions.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "qsa_internal.h"
+#include "qsa_layer.h"
+#include "qsa_ptx.cuh"
+
+namespace qsa {
+
+#define QSA_REJECT(status, ...)     \
+  do {                              \
+    qsa::set_error_detail(__VA_ARGS__); \
+    return status;                  \
+  } while (0)
+
+inline bool aligned_to(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+// a stride of `elem`-byte elements: non-negative and a multiple of `bytes`
+inline bool stride_multiple(int64_t s, int64_t elem, int64_t bytes) {
+  return s >= 0 && s <= INT64_MAX / 16 && (s * elem) % bytes == 0;
+}
+
+// The status of a launch sequence: reports the runtime's error and clears it.
+inline qsa_status_t launch_status(cudaError_t e, const char* what) {
+  if (e == cudaSuccess) return QSA_OK;
+  set_error_detail("%s: %s", what, cudaGetErrorString(e));
+  (void)cudaGetLastError();
+  return QSA_ERR_CUDA;
+}
+
+// D = A(16x32, row) * B(32x8, col) + D, int8 inputs, int32 accumulators.
+__device__ __forceinline__ void mma_s8_16832(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};\n"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Eight bf16 values from 16 bytes.
+__device__ __forceinline__ void bf16x8_to_f32(const uint4& r, float (&x)[8]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = bf16lo_to_f32(w[i]);
+    x[2 * i + 1] = bf16hi_to_f32(w[i]);
+  }
+}
+
+__device__ __forceinline__ uint4 f32_to_bf16x8(const float (&x)[8]) {
+  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                    pack_bf16x2(x[6], x[7]));
+}
+
+// Two floats -> two E4M3 codes (round to nearest even, saturated); `lo` in the low byte.
+__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// int8 codes of eight values over a scale: the value's quotient rounded half to even
+// (IEEE division, so every caller gets the same codes); zeros when the scale is not a
+// positive finite number.
+__device__ __forceinline__ uint2 int8x8_codes(const float (&x)[8], float scale) {
+  uint32_t w[2] = {0u, 0u};
+  if (scale > 0.f && scale < __builtin_huge_valf()) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      w[i >> 2] |= (uint32_t(__float2int_rn(__fdiv_rn(x[i], scale))) & 0xffu) << (8 * (i & 3));
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// max |x| that keeps a NaN (as NaN).
+__device__ __forceinline__ float nan_max(float a, float b) {
+  return (a != a || b != b) ? __int_as_float(0x7fffffff) : fmaxf(a, b);
+}
+
+}  // namespace qsa
