@@ -32,8 +32,9 @@ extern "C" {
 #define QSA_MAX_INDEX_HEADS 64
 #define QSA_MAX_TOP_BLOCKS 8192
 
-/* A further bit of *err_word: a bounded wait of qsa_paged_decode for its own copies ran out
- * (the device was stopped or is failing); the output is not valid. */
+/* A further bit of *err_word: a bounded wait of qsa_select_slots or qsa_paged_decode for its
+ * own copies or products ran out (the device was stopped or is failing); the output is not
+ * valid. */
 #define QSA_ERRBIT_TIMEOUT 0x10u
 
 /*
@@ -135,7 +136,7 @@ qsa_status_t qsa_pack_index_keys(const void* keys, int64_t key_stride_s, const i
  *   workspace   qsa_select_slots_workspace_bytes(...) bytes, 256-byte aligned.
  */
 size_t qsa_select_slots_workspace_bytes(int32_t Tq, int32_t B, int32_t P, int32_t page_size,
-                                        int32_t block);
+                                        int32_t Hi, int32_t Di, int32_t block);
 qsa_status_t qsa_select_slots(const void* q, int64_t q_stride_t, int64_t q_stride_h,
                               const float* weight, int64_t weight_stride, const int8_t* codes,
                               int64_t code_stride, const float* scales, const int32_t* page_table,

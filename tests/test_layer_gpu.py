@@ -322,7 +322,7 @@ def test_select_lengths_and_offsets_outside_their_range():
 def test_select_many_rows_in_chunks():
     """More rows than a chunk of scores holds, short sequences in a wide page table."""
     c = select_case(44, [1500, 700], [1100, 120], 1, 64, 4, 64, extra_pages=1000)
-    assert qsa.qsa_select_slots_workspace_bytes(1220, 2, 1024, 64, 4) == 64 << 20
+    assert qsa.qsa_select_slots_workspace_bytes(2, 2, 1024, 64, 1, 64, 4) == 2 * 16384 * 4
     assert c["page_table"].shape[1] > 1000
     check_select(c, 32)
 
@@ -623,3 +623,55 @@ def test_wrapper_refusals_on_the_gpu():
         qsa.qk_norm_rope(r["q"], r["positions"].expand(2, 4).contiguous(), r["inv_freq"])
     with pytest.raises(ValueError, match="k_cache"):
         qsa.qk_norm_rope(r["q"], r["positions"], r["inv_freq"], slots=r["positions"])
+
+
+# ---- selection: rows longer than the shared memory of the choice -----------------------------
+
+def keyed_case(score, rows, top, block=1):
+    """`rows` rows of one sequence whose blocks score `score` [n] (a positive scale each, dots of 1)."""
+    n = score.numel()
+    page = 64 * block
+    P = -(-n // 64) + 1
+    g = gen(90)
+    c = dict(block=block, page_size=page, cu_q=torch.tensor([0, rows], dtype=I32, device="cuda"))
+    c["page_table"] = torch.randperm(P, generator=g, device="cuda").to(I32).view(1, P)
+    c["seq_lens"] = torch.tensor([n * block], dtype=I32, device="cuda")
+    c["q"] = torch.zeros(rows, 1, 64, dtype=BF, device="cuda")
+    c["q"][:, :, 0] = 127.0
+    c["weight"] = torch.ones(rows, 1, device="cuda")
+    c["codes"] = torch.zeros(P * 64, 64, dtype=torch.int8, device="cuda")
+    c["codes"][:, 0] = 1
+    c["scales"] = torch.zeros(P * 64, device="cuda")
+    j = torch.arange(n, device="cuda")
+    c["scales"][c["page_table"][0, j // 64].long() * 64 + j % 64] = score
+    return c
+
+
+@pytest.mark.parametrize("rows", [1, 200, 700])
+@pytest.mark.parametrize("kind", ["random", "rising", "falling", "periodic", "two_values", "equal", "spread", "last"])
+def test_select_order_of_a_long_row(kind, rows):
+    """Scores that a sample of the row represents well, badly or not at all; one thread block per
+    row of every size (few rows, more than the SMs, many)."""
+    n = 40000
+    x = torch.rand(n, generator=gen(91), device="cuda") + 0.5
+    if kind in ("rising", "falling"):
+        x = x.sort(descending=kind == "falling").values
+    elif kind == "periodic":
+        x[torch.arange(n, device="cuda") % 39 == 0] += 5
+    elif kind == "two_values":
+        x = torch.where(x > 1.3, 2.0, 1.0)
+    elif kind == "equal":
+        x.fill_(1.0)
+    elif kind == "spread":  # over the whole range of exponents
+        x = torch.exp2((x - 1) * 250)
+    elif kind == "last":
+        x[:-700] = 0
+    c = keyed_case(x, rows, 0)
+    for top, sink, local in ((512, 0, 0), (512, 1, 7), (1, 0, 0), (3000, 0, 100)):
+        got, width = run_select(c, top, sink, local)
+        for t in (0, rows // 2, rows - 1):
+            one = dict(c, q=c["q"][t:t + 1], weight=c["weight"][t:t + 1], cu_q=None,
+                       seq_lens=c["seq_lens"] - (rows - 1 - t))
+            want, want_width = ref.select(one["q"], one["weight"], c["codes"], c["scales"], c["page_table"],
+                                          one["seq_lens"], None, top, c["page_size"], 1, sink, local)
+            assert torch.equal(got[t].cpu(), torch.from_numpy(want[0])) and int(width[t]) == int(want_width[0])

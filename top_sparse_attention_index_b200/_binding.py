@@ -71,7 +71,7 @@ SIGNATURES = {
                                 _i32, _i32, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _p,
                                 _i64, _i32, _f, _f, _p, _p]),
     "qsa_pack_index_keys": (_i32, [_p, _i64, _p, _i32, _i32, _i32, _i64, _p, _i64, _p, _p, _p]),
-    "qsa_select_slots_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32]),
+    "qsa_select_slots_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32, _i32]),
     "qsa_select_slots": (_i32, [_p, _i64, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _p, _p, _i32,
                                 _i32, _i32, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _p,
                                 _i64, _p, _p, _sz, _p, _p]),

@@ -13,8 +13,6 @@ constexpr int kStages = 2;
 constexpr int kSub = 16;                 // slots of a warp's sub-tile (the M of one MMA)
 constexpr int kMinSplit = 64;            // slots: what a thread block has in flight at once
 constexpr int kJoinThreads = 256;
-constexpr uint32_t kPolls = 64;           // polls of a wait between two looks at the clock
-constexpr uint64_t kWaitNs = 1000000000;  // bound of a wait for a sub-tile
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kRescaleLog2 = 8.0f;
 
@@ -36,30 +34,6 @@ __device__ __forceinline__ int tokens_of(const DecodeParams& p, int b, bool repo
   const int n = p.lens[b];
   if (report && p.err_word != nullptr && (n < 0 || n > most)) atomicOr(p.err_word, QSA_ERRBIT_WIDTH_RANGE);
   return int(min(int64_t(max(n, 0)), most));
-}
-
-// Bulk copy of one cache row to shared memory, completing on an mbarrier; both addresses
-// 16-byte aligned, the size a multiple of 16.  This device's memory, no multicast.
-__device__ __forceinline__ void bulk_row(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
-      "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
-      : "memory");
-}
-
-__device__ __forceinline__ uint64_t clock_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %globaltimer;\n" : "=l"(t));
-  return t;
-}
-
-// Waits for a phase of an mbarrier, one second at most; false when it has not come by then.
-__device__ __forceinline__ bool wait_rows(uint32_t bar, uint32_t parity) {
-  if (mbar_wait(bar, parity, kPolls)) return true;
-  const uint64_t start = clock_ns();
-  while (clock_ns() - start < kWaitNs)
-    if (mbar_wait(bar, parity, kPolls)) return true;
-  return false;
 }
 
 // NT n8 tiles hold the G heads of a KV head.  Rows in shared memory are padded by 16 bytes,
@@ -139,7 +113,7 @@ __global__ void __launch_bounds__(kDecodeThreads) qsa_paged_decode_kernel(const 
     if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(__popc(mask)) * 2 * C::kRow);
     __syncwarp();
     if (ok)
-      bulk_row(ring + stage * C::kStageBytes + lane * C::kPitch,
+      bulk_copy(ring + stage * C::kStageBytes + lane * C::kPitch,
                lane < 16 ? kg + slot * p.k_ss : vg + slot * p.v_ss, C::kRow, bar);
   };
 #pragma unroll
@@ -185,7 +159,7 @@ __global__ void __launch_bounds__(kDecodeThreads) qsa_paged_decode_kernel(const 
   for (int sub = warp; sub < subs; sub += kDecodeWarps) {
     const uint32_t kbuf = ring + stage * C::kStageBytes, vbuf = kbuf + kSub * C::kPitch;
     const uint32_t mask = stage == 0 ? valid[0] : valid[1];
-    if (__any_sync(0xffffffffu, !wait_rows(bars + stage * 8, phase))) {
+    if (__any_sync(0xffffffffu, !wait_phase(bars + stage * 8, phase))) {
       late = true;
       break;
     }
@@ -335,8 +309,8 @@ __global__ void __launch_bounds__(kDecodeThreads) qsa_paged_decode_kernel(const 
   }
   if (late) {  // give the copies in flight a second chance to land, then leave without a result
     if (lane == 0 && p.err_word != nullptr) atomicOr(p.err_word, QSA_ERRBIT_TIMEOUT);
-    wait_rows(bars + stage * 8, phase);
-    wait_rows(bars + (stage ^ 1) * 8, phase ^ uint32_t(stage));
+    wait_phase(bars + stage * 8, phase);
+    wait_phase(bars + (stage ^ 1) * 8, phase ^ uint32_t(stage));
   }
   if (__syncthreads_or(late)) return;
 

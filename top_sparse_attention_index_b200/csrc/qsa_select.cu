@@ -14,7 +14,6 @@ using namespace qsa;
 
 constexpr int kKeyTile = 128;                 // micro-blocks per tile: 16 per warp
 constexpr int kScoreThreads = 256;
-constexpr int kChooseThreads = 512;
 constexpr int64_t kChunkBytes = 64 << 20;     // keys of one chunk of rows
 constexpr int kMinChunkRows = 64;
 
@@ -30,6 +29,10 @@ struct SelectParams {
   int64_t q_st, q_sh, w_st, code_st, table_st, out_st, pages, ld;
   int32_t c0, c1;      // the chunk's rows
   int32_t Tq, B, P, page_size, per_page, Hi, block, top, sink, local;
+  int4* tiles;         // tcgen05 form: tiles of rows [chunks, max_tiles], and their codes and gains
+  uint8_t* tile_q;
+  int32_t cap, window;              // keys of a row, and words of its marks, in the choice's shared memory
+  uint32_t page_magic, block_magic; // 2^32 / per_page (/ block), rounded up
   int32_t chunk_tiles, chunks;  // score kernel: key tiles of a thread block, blocks of a row tile
 };
 
@@ -265,34 +268,560 @@ __global__ void __launch_bounds__(kScoreThreads) qsa_select_score_kernel(const S
   }
 }
 
+// ---- the score of many rows: tcgen05 -------------------------------------------------------
+
+// A tile is 128 micro-blocks (the rows of the accumulator) by 256 columns, which are
+// 256 / HP query rows of HP heads (HP: the heads rounded up to a power of two; missing ones
+// have gain 0).  Column (r / 2) 2 HP + 2 h + r mod 2 is head h of row r: a lane of the
+// accumulator holds one block's dots with all rows and heads, so the heads are added in order
+// within a thread, two rows per packed instruction.
+constexpr int kWideCols = 256;
+constexpr int kWideStages = 6;                     // key tiles in shared memory
+constexpr int kWideQ = 3;                          // Q tiles in shared memory (one more than a producer's lag)
+constexpr int kWideLag = 2;                        // tiles a producer has in flight behind the one it issues
+constexpr int kEpilogueWarps = 8, kProducerWarps = 4;
+constexpr int kWideThreads = 32 * (kEpilogueWarps + kProducerWarps + 1);
+
+__host__ __device__ constexpr int wide_tile_bytes(int DI) { return kWideCols * (DI + 4); }  // codes, then gains
+
+struct WideTile {
+  int b, t0, n, f;  // sequence, first row, rows, blocks to score (0: every row takes all its blocks)
+};
+__device__ __forceinline__ int tile_units(int f) { return (f + kKeyTile - 1) / kKeyTile; }
+
+// The tile'th tile of the chunk [c0, c1): sequences in order, each cut into tiles of `rows`
+// rows.  Called by a whole thread block; b = -1 past the last one.  `sh`: 4 ints.
+template <int THREADS>
+__device__ WideTile find_tile(const SelectParams& p, int c0, int c1, int tile, int rows, int* tmp, int* sh) {
+  const int tid = threadIdx.x;
+  if (tid == 0) sh[0] = -1;
+  __syncthreads();
+  int base = 0;
+  for (int b0 = 0; b0 < p.B; b0 += THREADS) {
+    int2 r = make_int2(0, 0);
+    if (b0 + tid < p.B) r = rows_of(p, b0 + tid, false);
+    r.x = max(r.x, c0);
+    r.y = min(r.y, c1);
+    const int mine = r.y > r.x ? (r.y - r.x + rows - 1) / rows : 0;
+    int total;
+    const int before = base + block_scan<THREADS>(mine, tmp, total) - mine;
+    if (tile >= before && tile < before + mine) {
+      const int t0 = r.x + (tile - before) * rows;
+      sh[0] = b0 + tid, sh[1] = t0, sh[2] = min(rows, r.y - t0);
+    }
+    base += total;
+    __syncthreads();
+    if (tile < base) break;
+  }
+  WideTile w{sh[0], sh[1], sh[2], 0};
+  if (w.b >= 0) {
+    const int last = rows_of(p, w.b, false).y - 1, len = length_of(p, w.b, false);
+    const int f_most = max(len - (last - (w.t0 + w.n - 1)), 0) / p.block;
+    w.f = f_most <= p.top ? 0 : f_most;
+  }
+  return w;
+}
+
+// The codes and gains of every tile's rows, laid out as the MMA reads them (no swizzle: 8
+// columns by 16 bytes contiguous), and the list of tiles: blockIdx.x is the tile, blockIdx.y
+// the chunk of rows.
+template <int DI, int HP>
+__global__ void __launch_bounds__(256) qsa_select_prep_kernel(const SelectParams p, int chunk_rows) {
+  constexpr int kLanes = DI / 8, kVec = 32 / kLanes;
+  __shared__ int sTmp[8], sFound[4];
+  const int c0 = int(min(int64_t(blockIdx.y) * chunk_rows, int64_t(p.Tq)));
+  const int c1 = int(min(int64_t(c0) + chunk_rows, int64_t(p.Tq)));
+  const WideTile w = find_tile<256>(p, c0, c1, blockIdx.x, kWideCols / HP, sTmp, sFound);
+  const int64_t slot = int64_t(blockIdx.y) * gridDim.x + blockIdx.x;
+  if (threadIdx.x == 0) p.tiles[slot] = make_int4(w.b, w.t0, w.n, w.b < 0 ? 0 : w.f);
+  if (w.b < 0 || w.f == 0) return;
+  uint8_t* dst = p.tile_q + slot * wide_tile_bytes(DI);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % kLanes;
+  constexpr int kRounds = kWideCols / (8 * kVec);  // vectors of a thread
+  constexpr int kAhead = kRounds < 4 ? kRounds : 4;
+  for (int i0 = 0; i0 < kRounds; i0 += kAhead) {
+    uint4 raw[kAhead];
+    float gain[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int v = ((i0 + u) * 8 + warp) * kVec + lane / kLanes;  // column
+      const int row = v / (2 * HP) * 2 + (v & 1), head = (v % (2 * HP)) >> 1;
+      raw[u] = make_uint4(0u, 0u, 0u, 0u);
+      gain[u] = 0.f;
+      if (row < w.n && head < p.Hi) {
+        raw[u] = __ldg(reinterpret_cast<const uint4*>(p.q + (w.t0 + row) * p.q_st + head * p.q_sh + l * 8));
+        gain[u] = __ldg(p.weight + (w.t0 + row) * p.w_st + head);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int v = ((i0 + u) * 8 + warp) * kVec + lane / kLanes;
+      const int row = v / (2 * HP) * 2 + (v & 1), head = (v % (2 * HP)) >> 1;
+      float xs[8], top = 0.f;
+      bf16x8_to_f32(raw[u], xs);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = nan_max(top, fabsf(xs[e]));
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) top = nan_max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      float scale = __fdiv_rn(top, 127.f);
+      if (!(scale < __builtin_huge_valf())) scale = __int_as_float(0x7fffffff);
+      const int c = l >> 1;
+      *reinterpret_cast<uint2*>(dst + (c >> 1) * (kWideCols * 32) + (v >> 3) * 256 + (c & 1) * 128 + (v & 7) * 16 +
+                                (l & 1) * 8) = int8x8_codes(xs, scale);
+      if (l == 0)
+        reinterpret_cast<float*>(dst + kWideCols * DI)[v] =
+            row < w.n && head < p.Hi ? __fmul_rn(gain[u], scale) : 0.f;
+    }
+  }
+}
+
+// Shared-memory matrix descriptor of a K-major tile of 8-row, 16-byte core matrices without
+// swizzle: 128 bytes between the two 16-byte halves of a 32-byte K step, 256 between 8-row
+// groups; instruction descriptor of kind::i8: signed A and B, 32-bit integer accumulator.
+__device__ __forceinline__ uint64_t core_desc(uint32_t addr) {
+  return uint64_t((addr >> 4) & 0x3FFFu) | (uint64_t(128 >> 4) << 16) | (uint64_t(256 >> 4) << 32) | (uint64_t(1) << 46);
+}
+constexpr uint32_t kI8Desc = (2u << 4) | (1u << 7) | (1u << 10) | (uint32_t(kWideCols >> 3) << 17) |
+                             (uint32_t(kKeyTile >> 4) << 24);
+
+__device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+
+template <int DI>
+struct Wide {
+  static constexpr int kKeyBytes = kKeyTile * DI;
+  static constexpr int kQBytes = wide_tile_bytes(DI);
+  // key stages, Q tiles, the stages' scales and valid marks
+  static constexpr int kSmem = kWideStages * kKeyBytes + kWideQ * kQBytes + kWideStages * kKeyTile * 8;
+};
+
+// One thread block per SM walks an equal share of all (tile of rows, tile of keys) pairs.
+// Four warps bring key tiles in (16-byte asynchronous copies through the page table, a
+// stage ahead of their page lookups), one thread issues the MMAs into two accumulators, eight
+// warps turn dots into keys.  What bounds it is those warps' integer and float
+// instructions: per pair of dots an add-with-maximum each (the integer to float conversion
+// 2^23 + max(d, 0) and the clamp at once; a dot of 128 codes is below 2^21), and a packed
+// subtraction, product and sum.
+template <int DI, int HP>
+__global__ void __launch_bounds__(kWideThreads, 1)
+    qsa_select_wide_kernel(const SelectParams p, const int4* tiles, const uint8_t* tile_q, int max_tiles) {
+  using C = Wide<DI>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sQ = smem + kWideStages * C::kKeyBytes;
+  float* sScale = reinterpret_cast<float*>(sQ + kWideQ * C::kQBytes);             // [stages][128]
+  int* sValid = reinterpret_cast<int*>(sScale + kWideStages * kKeyTile);     // [stages][128]
+  // key stage full / free, Q full / free, accumulator full / free
+  __shared__ __align__(8) uint64_t sBar[2 * kWideStages + 2 * kWideQ + 4];
+  __shared__ uint32_t sTmem;
+  __shared__ int sTmp[kWideThreads / 32], sStart[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto bar = [&](int i) { return smem_addr(sBar + i); };
+  constexpr int kFull = 0, kFree = kWideStages, kQFull = 2 * kWideStages, kQFree = kQFull + kWideQ,
+                kAccFull = kQFree + kWideQ, kAccFree = kAccFull + 2;
+
+  // ---- this block's share ------------------------------------------------------------------
+  int64_t total_units = 0;
+  for (int i0 = 0; i0 < max_tiles; i0 += kWideThreads) {
+    int total;
+    block_scan<kWideThreads>(i0 + tid < max_tiles ? tile_units(tiles[i0 + tid].w) : 0, sTmp, total);
+    total_units += total;
+  }
+  const int64_t u0 = total_units * blockIdx.x / gridDim.x, u1 = total_units * (blockIdx.x + 1) / gridDim.x;
+  if (u0 == u1) return;
+  int64_t base = 0;
+  for (int i0 = 0; i0 < max_tiles; i0 += kWideThreads) {
+    const int mine = i0 + tid < max_tiles ? tile_units(tiles[i0 + tid].w) : 0;
+    int total;
+    const int64_t before = base + block_scan<kWideThreads>(mine, sTmp, total) - mine;
+    if (u0 >= before && u0 < before + mine) sStart[0] = i0 + tid, sStart[1] = int(u0 - before);
+    base += total;
+    if (base > u0) break;  // (uniform)
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kWideStages; ++i) {
+      mbar_init(bar(kFull + i), 32 * kProducerWarps);
+      mbar_init(bar(kFree + i), 1 + kEpilogueWarps);
+    }
+    for (int i = 0; i < kWideQ; ++i) {
+      mbar_init(bar(kQFull + i), 1);
+      mbar_init(bar(kQFree + i), 1 + kEpilogueWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kAccFull + i), 1);
+      mbar_init(bar(kAccFree + i), kEpilogueWarps);
+    }
+    mbar_init_fence();
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sTmem)), "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::);
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = sTmem;
+  const int tile0 = sStart[0], first_kt = sStart[1];
+  const int share = int(u1 - u0);
+  bool late = false;
+
+  if (warp >= kEpilogueWarps && warp < kEpilogueWarps + kProducerWarps) {
+    // ---- producers: one key row per thread -----------------------------------------------------
+    const int r = tid - 32 * kEpilogueWarps;
+    int tile = tile0, kt = first_kt, qn = 0;  // qn: Q tiles issued
+    bool new_q = true;
+    int4 w = tiles[tile];
+    // of this thread's row of key tile kt of w: the page as the table has it, the block within
+    // it, and whether there is such a block (used one step later, when the load has arrived)
+    int page = -1, off = 0;
+    bool live = false;
+    auto lookup = [&]() {
+      const int j = kt * kKeyTile + r;
+      live = j < w.w;
+      if (!live) return;
+      int m = j;
+      if (p.per_page > 1) {
+        m = __umulhi(uint32_t(j), p.page_magic);
+        if (int64_t(m) * p.per_page > j) --m;
+      }
+      off = j - m * p.per_page;
+      page = __ldg(p.table + w.x * p.table_st + m);
+    };
+    lookup();
+    const uint32_t row_s = smem_addr(smem) + (r >> 3) * 256 + (r & 7) * 16;
+    for (int i = 0; i < share; ++i) {
+      const bool ok = live && page >= 0 && page < p.pages, bad = live && !ok;
+      const int64_t phys = ok ? int64_t(page) * p.per_page + off : 0;
+      const bool load_q = new_q;
+      const int this_tile = tile;
+      new_q = false;
+      if (++kt == tile_units(w.w)) {
+        kt = 0;
+        new_q = true;
+        do ++tile; while (tile < max_tiles && tiles[tile].w == 0);
+        if (tile < max_tiles) w = tiles[tile];
+      }
+      if (i + 1 < share) lookup();
+      const int stage = i % kWideStages;
+      if (i >= kWideStages && !wait_phase(bar(kFree + stage), (i / kWideStages - 1) & 1)) late = true;
+      if (load_q) {
+        const int qb = qn % kWideQ;
+        if (r == 0 && !late) {
+          if (qn >= kWideQ && !wait_phase(bar(kQFree + qb), (qn / kWideQ - 1) & 1)) late = true;
+          if (!late) {
+            mbar_arrive_expect_tx(bar(kQFull + qb), C::kQBytes);
+            bulk_copy(smem_addr(sQ) + qb * C::kQBytes, tile_q + int64_t(this_tile) * C::kQBytes, C::kQBytes,
+                      bar(kQFull + qb));
+          }
+        }
+        if (!late) ++qn;
+      }
+      if (late) break;
+      if (bad && p.err_word != nullptr) atomicOr(p.err_word, QSA_ERRBIT_SLOT_RANGE);
+      const int8_t* src = p.codes + phys * p.code_st;
+      const uint32_t dst = row_s + stage * C::kKeyBytes;
+#pragma unroll
+      for (int c = 0; c < DI / 16; ++c)
+        cp_async_16(dst + (c >> 1) * (kKeyTile * 32) + (c & 1) * 128, ok ? src + c * 16 : src, ok);
+      sValid[stage * kKeyTile + r] = !bad;
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(smem_addr(sScale + stage * kKeyTile + r)),
+                   "l"(p.scales + phys), "r"(ok ? 4 : 0)
+                   : "memory");
+      cp_async_commit();
+      if (i >= kWideLag) {  // the tile issued kWideLag before has landed: hand it over
+        cp_async_wait<kWideLag>();
+        fence_proxy_async_smem();
+        mbar_arrive(bar(kFull + (i - kWideLag) % kWideStages));
+      }
+    }
+    cp_async_wait<0>();
+    fence_proxy_async_smem();
+    if (!late)
+      for (int i = max(share - kWideLag, 0); i < share; ++i) mbar_arrive(bar(kFull + i % kWideStages));
+    if (r == 0)  // no copy in flight
+      for (int i = max(qn - kWideQ, 0); i < qn; ++i) late |= !wait_phase(bar(kQFull + i % kWideQ), (i / kWideQ) & 1);
+  } else if (warp == kEpilogueWarps + kProducerWarps) {
+    // ---- one thread issues the MMAs ------------------------------------------------------------
+    if (lane == 0) {
+      int kt = first_kt, tile = tile0, units = tile_units(tiles[tile0].w), qn = 0;
+      bool new_q = true;
+      int i = 0;
+      for (; i < share; ++i) {
+        const int stage = i % kWideStages, acc = i & 1;
+        if (new_q) late = !wait_phase(bar(kQFull + qn % kWideQ), (qn / kWideQ) & 1);
+        if (!late) late = !wait_phase(bar(kFull + stage), (i / kWideStages) & 1);
+        if (!late && i >= 2) late = !wait_phase(bar(kAccFree + acc), ((i >> 1) - 1) & 1);
+        if (late) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t a = smem_addr(smem) + stage * C::kKeyBytes, q = smem_addr(sQ) + (qn % kWideQ) * C::kQBytes;
+#pragma unroll
+        for (int k = 0; k < DI / 32; ++k)
+          asm volatile(
+              "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+              "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(tmem + acc * kWideCols),
+              "l"(core_desc(a + k * (kKeyTile * 32))), "l"(core_desc(q + k * (kWideCols * 32))), "r"(kI8Desc),
+              "r"(uint32_t(k != 0)));
+        auto commit = [&](int b) {
+          asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar(b))
+                       : "memory");
+        };
+        commit(kAccFull + acc);
+        commit(kFree + stage);
+        new_q = false;
+        if (++kt == units) {
+          commit(kQFree + qn % kWideQ);
+          ++qn;
+          kt = 0;
+          new_q = true;
+          do ++tile; while (tile < max_tiles && tiles[tile].w == 0);
+          units = tile < max_tiles ? tile_units(tiles[tile].w) : 0;
+        }
+      }
+      if (i > 0) late |= !wait_phase(bar(kAccFull + ((i - 1) & 1)), ((i - 1) >> 1) & 1);  // no MMA in flight
+    }
+  } else {
+    // ---- dots to keys --------------------------------------------------------------------------
+    const int quad = warp & 3, half = warp >> 2;  // lanes of the accumulator, half of its columns
+    const int r = quad * 32 + lane;
+    constexpr int kHalfRows = kWideCols / 2 / HP;
+    int tile = tile0, kt = first_kt, qn = 0;
+    int4 w = tiles[tile];
+    for (int i = 0; i < share; ++i) {
+      const int stage = i % kWideStages, acc = i & 1;
+      // (the key stage and the Q tile landed before their product: these waits order the reads)
+      bool here = wait_phase(bar(kAccFull + acc), (i >> 1) & 1);
+      here = here && wait_phase(bar(kFull + stage), (i / kWideStages) & 1) &&
+             wait_phase(bar(kQFull + qn % kWideQ), (qn / kWideQ) & 1);
+      if (__any_sync(0xffffffffu, !here)) {
+        late = true;
+        break;
+      }
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const float scale = sScale[stage * kKeyTile + r];
+      const bool valid = sValid[stage * kKeyTile + r] != 0;
+      const bool any_bad = __any_sync(0xffffffffu, !valid);
+      const int j = kt * kKeyTile + r;
+      const uint64_t scale2 = pack2(scale, scale);
+      const float* gains = reinterpret_cast<const float*>(sQ + (qn % kWideQ) * C::kQBytes + kWideCols * DI) + half * 128;
+      const int row0 = half * kHalfRows;
+      uint32_t* out = p.keys + int64_t(w.y + row0 - p.c0) * p.ld + j;
+      const bool store = j < p.ld;
+      const uint64_t minus = pack2(-8388608.f, -8388608.f), zero = pack2(0.f, 0.f);
+      uint64_t sum = zero;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t d[32];
+        tmem_ld32(d, tmem + acc * kWideCols + half * 128 + c * 32 + (uint32_t(quad * 32) << 16));
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+        if (c == 3) {  // the accumulator has been read
+          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kAccFree + acc));
+        }
+#pragma unroll
+        for (int x = 0; x < 32; x += 4) {  // two heads of a pair of rows (HP = 1: two pairs of rows)
+          const float4 g = *reinterpret_cast<const float4*>(gains + c * 32 + x);
+          float f[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f[e] = __int_as_float(__viaddmax_s32(int(d[x + e]), 0x4B000000, 0x4B000000));
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int col = c * 32 + x + 2 * e, head = (col % (2 * HP)) >> 1, pair = col / (2 * HP);
+            const uint64_t term = mul2(add2(pack2(f[2 * e], f[2 * e + 1]), minus),
+                                       e == 0 ? pack2(g.x, g.y) : pack2(g.z, g.w));
+            sum = head == 0 ? term : add2(sum, term);
+            if (head == HP - 1) {
+              float s[2];
+              unpack2(fma2(sum, scale2, zero), s[0], s[1]);  // (-0 becomes +0)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t u = __float_as_uint(fmaxf(s[k], -__builtin_huge_valf()));  // NaN: -infinity
+                uint32_t key = u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
+                if (any_bad && !valid) key = 0u;
+                if (store && row0 + 2 * pair + k < w.z) *out = key;
+                out += p.ld;
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kFree + stage));
+      if (++kt == tile_units(w.w)) {
+        if (lane == 0) mbar_arrive(bar(kQFree + qn % kWideQ));
+        ++qn;
+        kt = 0;
+        do ++tile; while (tile < max_tiles && tiles[tile].w == 0);
+        if (tile < max_tiles) w = tiles[tile];
+      }
+    }
+  }
+  if (late && p.err_word != nullptr) atomicOr(p.err_word, QSA_ERRBIT_TIMEOUT);
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+}
+
 // ---- the choice --------------------------------------------------------------------------
 
-// One thread block per row.  Three radix passes over the row's keys (11, 11 and 10 bits,
-// highest first) find the key of the top-th block and how many blocks of exactly that key
-// belong to it; a scan in block order then collects the taken blocks.
-__global__ void __launch_bounds__(kChooseThreads) qsa_select_choose_kernel(const SelectParams p) {
-  extern __shared__ int sList[];  // [min(top, blocks)] first physical slot of each taken block, or -1
-  __shared__ int sHist[2048];
-  __shared__ int sTmp[kChooseThreads / 32], sPick[2], sSeq;
-  const int tid = threadIdx.x;
+constexpr int kBins = 512;     // of a histogram: 16 per lane of one warp
+constexpr int kSample = 1024;  // keys that estimate the border of a long row
+constexpr int kBatch = 4;      // 16-byte loads of keys in flight per thread
+constexpr int kWindow = 1024;  // most words of the marks: 32,768 blocks at a time
+
+// The border of a row: blocks of a larger key are taken, of `equal` equal ones the first `want`.
+struct Border {
+  uint32_t key;
+  int want, equal;
+};
+
+struct ChooseShared {
+  int hist[kBins];
+  uint32_t few[32];
+  uint32_t lo, hi;
+  int n_few, bin, above, count, n;
+};
+
+// The want-th largest (1 <= want <= n) of the keys key_at(0 .. n - 1), by histograms of the
+// key range that still holds it; the last step ranks at most 32 keys within each warp.
+template <int THREADS, class F>
+__device__ Border kth_largest(int n, int want, F key_at, ChooseShared& sh) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  __syncthreads();  // (sh and the keys)
+  if (tid == 0) sh.lo = 0xffffffffu, sh.hi = 0u, sh.n_few = 0;
+  for (int i = tid; i < kBins; i += THREADS) sh.hist[i] = 0;
+  uint32_t lo = 0xffffffffu, hi = 0u;
+#pragma unroll 4
+  for (int i = tid; i < n; i += THREADS) {
+    const uint32_t k = key_at(i);
+    lo = min(lo, k);
+    hi = max(hi, k);
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  __syncthreads();
+  if (lane == 0 && lo <= hi) {
+    atomicMin(&sh.lo, lo);
+    atomicMax(&sh.hi, hi);
+  }
+  __syncthreads();
+  lo = sh.lo;
+  hi = sh.hi;
+  for (;;) {
+    const uint32_t range = hi - lo;
+    const int shift = range < uint32_t(kBins) ? 0 : 32 - __clz(range) - 9;  // 2^9 = kBins
+#pragma unroll 4
+    for (int i = tid; i < n; i += THREADS) {
+      const uint32_t k = key_at(i) - lo;
+      if (k <= range) atomicAdd(&sh.hist[k >> shift], 1);
+    }
+    __syncthreads();
+    if (tid < 32) {  // lane i holds bins 511 - 16 i down to 496 - 16 i
+      const int first = kBins - 16 * (lane + 1);
+      int c[16], mine = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int4 x = *reinterpret_cast<const int4*>(&sh.hist[first + 4 * e]);
+        c[4 * e] = x.x, c[4 * e + 1] = x.y, c[4 * e + 2] = x.z, c[4 * e + 3] = x.w;
+        mine += x.x + x.y + x.z + x.w;
+      }
+      int above = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, above, o);
+        if (lane >= o) above += y;
+      }
+      above -= mine;
+      if (above < want && above + mine >= want) {
+#pragma unroll
+        for (int e = 15; e >= 0; --e) {
+          if (above < want && above + c[e] >= want) sh.bin = first + e, sh.above = above, sh.count = c[e];
+          above += c[e];
+        }
+      }
+    }
+    __syncthreads();
+    want -= sh.above;
+    const int count = sh.count;
+    lo += uint32_t(sh.bin) << shift;
+    hi = lo + min(hi - lo, (1u << shift) - 1u);
+    if (shift == 0) return {lo, want, count};
+    if (count <= 32) {
+#pragma unroll 4
+      for (int i = tid; i < n; i += THREADS) {
+        const uint32_t k = key_at(i);
+        if (k - lo <= hi - lo) sh.few[atomicAdd(&sh.n_few, 1)] = k;
+      }
+      __syncthreads();
+      const uint32_t mine = sh.few[lane < count ? lane : 0];
+      int more = 0, same = 0;
+      for (int i = 0; i < count; ++i) {
+        const uint32_t k = __shfl_sync(0xffffffffu, mine, i);
+        more += k > mine;
+        same += k == mine;
+      }
+      const uint32_t at = __ballot_sync(0xffffffffu, lane < count && more < want && more + same >= want);
+      const int src = __ffs(at) - 1;
+      return {__shfl_sync(0xffffffffu, mine, src), want - __shfl_sync(0xffffffffu, more, src),
+              __shfl_sync(0xffffffffu, same, src)};
+    }
+    for (int i = tid; i < kBins; i += THREADS) sh.hist[i] = 0;
+    __syncthreads();
+  }
+}
+
+// One thread block per row.  A row of at most `cap` blocks has its keys in shared memory.  Of
+// a longer one, the keys above a border estimated from kSample of them are collected there
+// in one pass (the estimate leaves out too much, or not enough, for about one row in 10^6,
+// and for keys that repeat with the sample's period: such a row searches its keys in place).
+// The exact border follows from what was collected; a bit per block marks the taken ones,
+// and a scan over the marks gives them their places in ascending order.
+// Bound: the instructions over a row's keys and its output, with the keys read from L2 once
+// (radix passes over the whole row, four reads and a conflicting shared-memory atomic per key
+// and pass, took 165 us per 1,024 rows of 15,500 blocks).
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) qsa_select_choose_kernel(const SelectParams p) {
+  extern __shared__ __align__(16) uint32_t dyn[];
+  uint32_t* sKey = dyn;                                       // [cap]
+  int* sIdx = reinterpret_cast<int*>(sKey + p.cap);           // [cap], absent when every row fits
+  int* sList = sIdx + (p.ld > p.cap ? p.cap : 0);             // [top] first slot of each taken block, or -1
+  __shared__ __align__(16) ChooseShared sh;
+  uint32_t* sOver = reinterpret_cast<uint32_t*>(sList + (p.top + 3) / 4 * 4);  // [window] each
+  uint32_t* sSame = sOver + p.window;
+  __shared__ int sTmp[THREADS / 32], sSeq;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t = p.c0 + blockIdx.x;
   if (tid == 0) sSeq = (p.cu == nullptr && t < p.B) ? t : -1;
   __syncthreads();
-  if (p.cu != nullptr)
-    for (int i = tid; i < p.B; i += kChooseThreads) {
+  if (p.cu != nullptr) {
+    for (int i = tid; i < p.B; i += THREADS) {
       const int2 r = rows_of(p, i, blockIdx.x == 0 && p.c0 == 0);
       if (t >= r.x && t < r.y) atomicMax(&sSeq, i);  // (offsets that overlap: the last one)
     }
-  __syncthreads();
+    __syncthreads();
+  }
   const int b = sSeq;
   if (b < 0) return;
   const int last = rows_of(p, b, false).y - 1, len = length_of(p, b, tid == 0);
   const int seen = max(len - (last - t), 0);
   const int f = seen / p.block, taken = min(f, p.top);
   const uint32_t* row = p.keys + blockIdx.x * p.ld;
+  const int32_t* table = p.table + b * p.table_st;
   auto first_slot = [&](int j) {  // of block j, or -1
-    const int m = j / p.per_page;
-    const int page = __ldg(p.table + b * p.table_st + m);
+    int m = j;
+    if (p.per_page > 1) {
+      m = __umulhi(uint32_t(j), p.page_magic);  // j / per_page, or one more
+      if (int64_t(m) * p.per_page > j) --m;
+    }
+    const int page = __ldg(table + m);
     if (page < 0 || page >= p.pages) {
       if (p.err_word != nullptr) atomicOr(p.err_word, QSA_ERRBIT_SLOT_RANGE);
       return -1;
@@ -300,63 +829,145 @@ __global__ void __launch_bounds__(kChooseThreads) qsa_select_choose_kernel(const
     return page * p.page_size + (j - m * p.per_page) * p.block;
   };
   if (f <= p.top) {
-    for (int j = tid; j < f; j += kChooseThreads) sList[j] = first_slot(j);
+    for (int j = tid; j < f; j += THREADS) sList[j] = first_slot(j);
   } else {
-    auto key_of = [&](int j) { return (j < p.sink || j >= f - p.local) ? 0xffffffffu : row[j]; };
-    uint32_t prefix = 0, mask = 0;
-    int want = p.top;  // blocks still to be found among the keys that match the prefix
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-      const uint32_t digit = pass == 2 ? 0x3ffu : 0x7ffu;
-      for (int i = tid; i < 2048; i += kChooseThreads) sHist[i] = 0;
+    auto forced = [&](int j, uint32_t k) { return (j < p.sink || j >= f - p.local) ? 0xffffffffu : k; };
+    auto in_row = [&](int j) { return forced(j, __ldg(row + j)); };
+    const uint4* row4 = reinterpret_cast<const uint4*>(row);  // (ld is a multiple of 32)
+    auto in_list = [&](int i) { return sKey[i]; };
+    Border border;
+    int listed = -1;  // keys collected with their blocks; -1: every block of the row is searched
+    if (f <= p.cap) {
+      for (int i0 = tid; i0 * 4 < f; i0 += THREADS * kBatch) {
+        uint4 k[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+          if ((i0 + u * THREADS) * 4 < f) k[u] = __ldg(row4 + i0 + u * THREADS);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int j = (i0 + u * THREADS) * 4;
+          if (j >= f) break;
+          *reinterpret_cast<uint4*>(sKey + j) = make_uint4(forced(j, k[u].x), forced(j + 1, k[u].y),
+                                                           forced(j + 2, k[u].z), forced(j + 3, k[u].w));
+        }
+      }
+      border = kth_largest<THREADS>(f, p.top, in_list, sh);
+    } else {
+      {
+        uint32_t k[kSample / THREADS];  // one from each of kSample equal parts of the row
+#pragma unroll
+        for (int u = 0; u < kSample / THREADS; ++u) {
+          const uint32_t i = tid + u * THREADS;
+          k[u] = in_row(int((uint64_t(i) * uint32_t(f) + __umulhi(i * 2654435769u, uint32_t(f))) / kSample));
+        }
+#pragma unroll
+        for (int u = 0; u < kSample / THREADS; ++u) sKey[tid + u * THREADS] = k[u];
+      }
+      // of the row's `top` best, about `hits` are in the sample: the border lies 5 deviations lower
+      const float hits = float(p.top) * kSample / float(f);
+      const uint32_t low =
+          kth_largest<THREADS>(kSample, min(int(hits + 5.f * sqrtf(hits)) + 6, kSample), in_list, sh).key;
       __syncthreads();
-      for (int j = tid; j < f; j += kChooseThreads) {
-        const uint32_t k = key_of(j);
-        if ((k & mask) == prefix) atomicAdd(&sHist[(k >> shift) & digit], 1);
+      if (tid == 0) sh.n = 0;
+      __syncthreads();
+      const uint32_t below = (1u << lane) - 1u;
+      for (int i0 = warp * 32; i0 * 4 < f; i0 += THREADS * kBatch) {
+        uint4 raw[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          raw[u] = make_uint4(0u, 0u, 0u, 0u);
+          if ((i0 + lane + u * THREADS) * 4 < f) raw[u] = __ldg(row4 + i0 + lane + u * THREADS);
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int j = (i0 + lane + u * THREADS) * 4;
+          const uint32_t k[4] = {forced(j, raw[u].x), forced(j + 1, raw[u].y), forced(j + 2, raw[u].z),
+                                 forced(j + 3, raw[u].w)};
+          uint32_t keep[4];
+          int total = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            keep[e] = __ballot_sync(0xffffffffu, j + e < f && k[e] >= low);
+            total += __popc(keep[e]);
+          }
+          if (total == 0) continue;
+          int at = 0;
+          if (lane == 0) at = atomicAdd(&sh.n, total);
+          at = __shfl_sync(0xffffffffu, at, 0);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = at + __popc(keep[e] & below);
+            if (((keep[e] >> lane) & 1) && i < p.cap) sKey[i] = k[e], sIdx[i] = j + e;
+            at += __popc(keep[e]);
+          }
+        }
       }
       __syncthreads();
-      // thread i owns the bins 2047 - 4 i down to 2044 - 4 i: the scan runs from the top
-      int c[4], mine = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) mine += c[e] = sHist[2047 - 4 * tid - e];
-      int total;
-      int above = block_scan<kChooseThreads>(mine, sTmp, total) - mine;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (above < want && above + c[e] >= want) sPick[0] = 2047 - 4 * tid - e, sPick[1] = want - above;
-        above += c[e];
+      if (sh.n >= p.top && sh.n <= p.cap) {
+        listed = sh.n;
+        border = kth_largest<THREADS>(listed, p.top, in_list, sh);
+      } else {
+        border = kth_largest<THREADS>(f, p.top, in_row, sh);
       }
-      __syncthreads();
-      prefix |= uint32_t(sPick[0]) << shift;
-      mask |= digit << shift;
-      want = sPick[1];
-      __syncthreads();
     }
-    // blocks above `prefix` are taken, and the first `want` that equal it
+    // ---- marks and places, a window of blocks at a time ----------------------------------------
+    const bool all_same = border.want == border.equal;  // no choice between equal keys
     int have = 0, same = 0;
-    for (int j0 = 0; j0 < f; j0 += kChooseThreads) {
-      const int j = j0 + tid;
-      const uint32_t k = j < f ? key_of(j) : 0u;
-      const bool over = j < f && k > prefix, equal = j < f && k == prefix;
-      int total;
-      const int incl = block_scan<kChooseThreads>((over ? 1 : 0) | (equal ? 1 << 16 : 0), sTmp, total);
-      const int ties = same + (incl >> 16) - (equal ? 1 : 0);  // equal ones before this block
-      if (over || (equal && ties < want)) {
-        const int at = have + (incl & 0xffff) - (over ? 1 : 0) + min(ties, want);
-        sList[at] = first_slot(j);
+    for (int w0 = 0; w0 * 32 < f; w0 += p.window) {
+      const int words = min(p.window, (f + 31) / 32 - w0);
+      auto over = [&](uint32_t k) { return k > border.key || (all_same && k == border.key); };
+      if (listed >= 0) {
+        __syncthreads();  // (the last window's marks)
+        for (int i = tid; i < words; i += THREADS) sOver[i] = sSame[i] = 0u;
+        __syncthreads();
+        for (int i = tid; i < listed; i += THREADS) {
+          const uint32_t k = sKey[i];
+          const int j = sIdx[i], w = (j >> 5) - w0;
+          if (k >= border.key && w >= 0 && w < words) atomicOr(over(k) ? &sOver[w] : &sSame[w], 1u << (j & 31));
+        }
+      } else {
+        __syncthreads();
+        for (int w = warp; w < words; w += THREADS / 32) {
+          const int j = (w0 + w) * 32 + lane;
+          const uint32_t k = j < f ? (f <= p.cap ? sKey[j] : in_row(j)) : 0u;
+          const uint32_t o = __ballot_sync(0xffffffffu, j < f && over(k));
+          const uint32_t s = __ballot_sync(0xffffffffu, j < f && !all_same && k == border.key);
+          if (lane == 0) sOver[w] = o, sSame[w] = s;
+        }
       }
-      have += total & 0xffff;
-      same += total >> 16;
+      __syncthreads();
+      const int per = (words + THREADS - 1) / THREADS, first = tid * per, end = min(first + per, words);
+      int mine = 0, mine_same = 0;
+      for (int w = first; w < end; ++w) {
+        mine += __popc(sOver[w]);
+        mine_same += __popc(sSame[w]);
+      }
+      int total, total_same = 0;
+      int before = have + block_scan<THREADS>(mine, sTmp, total) - mine, before_same = same;
+      if (!all_same) before_same += block_scan<THREADS>(mine_same, sTmp, total_same) - mine_same;
+      for (int w = first; w < end; ++w) {
+        uint32_t o = sOver[w], any = o | sSame[w];
+        while (any != 0u) {
+          const int bit = __ffs(any) - 1;
+          any &= any - 1;
+          const bool is_over = (o >> bit) & 1;
+          if (is_over || before_same < border.want)
+            sList[before + (all_same ? 0 : min(before_same, border.want))] = first_slot((w0 + w) * 32 + bit);
+          if (is_over) ++before; else ++before_same;
+        }
+      }
+      have += total;
+      same += total_same;
     }
   }
   __syncthreads();
   int32_t* out = p.out + t * p.out_st;
   const int W = p.top * p.block + p.block - 1, full = taken * p.block, tail = seen - f * p.block;
   const int tail_slot = tail > 0 ? first_slot(f) : -1;
-  for (int w = tid; w < W; w += kChooseThreads) {
+  for (int w = tid; w < W; w += THREADS) {
     int s = -1;
     if (w < full) {
-      const int i = w / p.block;
+      const int i = p.block == 1 ? w : int(__umulhi(uint32_t(w), p.block_magic));  // w / block (w below 2^14)
       s = sList[i] < 0 ? -1 : sList[i] + (w - i * p.block);
     } else if (w < full + tail) {
       s = tail_slot < 0 ? -1 : tail_slot + (w - full);
@@ -401,6 +1012,59 @@ cudaError_t launch_score(SelectParams& p, int groups, int num_sms, cudaStream_t 
   return cudaGetLastError();
 }
 
+int heads_padded(int Hi) {
+  int hp = 1;
+  while (hp < Hi) hp *= 2;
+  return hp;
+}
+
+// The tcgen05 form pays once a tile's 256 columns are filled to a quarter on average.
+bool use_wide(int32_t Tq, int32_t B, int32_t Hi, bool has_cu) {
+  return has_cu && int64_t(Tq) * heads_padded(Hi) * 4 >= int64_t(B) * kWideCols;
+}
+
+int64_t wide_max_tiles(int32_t rows, int32_t B, int32_t Hi) {  // a sequence adds at most one partial tile
+  return rows / (kWideCols / heads_padded(Hi)) + (B < rows ? B : rows);
+}
+
+template <int DI, int HP>
+cudaError_t launch_prep(const SelectParams& p, int chunk_rows, int chunks, cudaStream_t st) {
+  const dim3 grid(unsigned(wide_max_tiles(chunk_rows, p.B, p.Hi)), unsigned(chunks));
+  qsa_select_prep_kernel<DI, HP><<<grid, 256, 0, st>>>(p, chunk_rows);
+  return cudaGetLastError();
+}
+
+template <int DI, int HP>
+cudaError_t launch_wide(const SelectParams& p, int chunk, int chunk_rows, int num_sms, cudaStream_t st) {
+  const cudaError_t e = cudaFuncSetAttribute(qsa_select_wide_kernel<DI, HP>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, Wide<DI>::kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t max_tiles = wide_max_tiles(chunk_rows, p.B, p.Hi);
+  qsa_select_wide_kernel<DI, HP><<<num_sms, kWideThreads, Wide<DI>::kSmem, st>>>(
+      p, p.tiles + chunk * max_tiles, p.tile_q + chunk * max_tiles * wide_tile_bytes(DI), int(max_tiles));
+  return cudaGetLastError();
+}
+
+// prep: the tiles of all chunks (chunk < 0), or the scores of one chunk
+template <int DI>
+cudaError_t launch_wide_for(const SelectParams& p, int chunk, int chunk_rows, int chunks, int num_sms, cudaStream_t st) {
+#define QSA_WIDE(HP)                                                       \
+  case HP:                                                                 \
+    return chunk < 0 ? launch_prep<DI, HP>(p, chunk_rows, chunks, st)      \
+                     : launch_wide<DI, HP>(p, chunk, chunk_rows, num_sms, st);
+  switch (heads_padded(p.Hi)) {
+    QSA_WIDE(1)
+    QSA_WIDE(2)
+    QSA_WIDE(4)
+    QSA_WIDE(8)
+    QSA_WIDE(16)
+    QSA_WIDE(32)
+    QSA_WIDE(64)
+    default: return cudaErrorInvalidValue;
+  }
+#undef QSA_WIDE
+}
+
 // One row per sequence fills a tile of four rows at most: the narrowest tile that holds all
 // heads.  Otherwise 64 columns.
 template <int DI>
@@ -414,7 +1078,54 @@ cudaError_t launch_score_for(SelectParams& p, int num_sms, cudaStream_t st) {
   return narrow ? launch_score<DI, 1, 1>(p, 1, num_sms, st) : launch_score<DI, 1, 8>(p, 1, num_sms, st);
 }
 
-qsa_status_t check_select_sizes(int32_t Tq, int32_t B, int32_t P, int32_t page_size, int32_t block) {
+// Many rows: small thread blocks, of which an SM holds many.  A row or a few per SM (a decode
+// step): the largest ones, since the row's own latency is the time.
+template <int THREADS>
+cudaError_t launch_choose_for(const SelectParams& p, size_t smem, cudaStream_t st) {
+  const cudaError_t e = cudaFuncSetAttribute(qsa_select_choose_kernel<THREADS>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e != cudaSuccess) return e;
+  qsa_select_choose_kernel<THREADS><<<p.c1 - p.c0, THREADS, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_choose(SelectParams& p, int num_sms, cudaStream_t st) {
+  // room for what the sample's border lets through: about 1.3 to 2 times `top` for long rows
+  const int want = p.top * 5 / 2 > 2048 ? p.top * 5 / 2 : 2048;
+  p.cap = int(p.ld < want ? (p.ld < kSample ? kSample : p.ld) : want) / 4 * 4;
+  p.window = p.ld / 32 < kWindow ? int(p.ld / 32) : kWindow;  // (ld is a multiple of 32)
+  const size_t smem = size_t(p.cap) * (p.ld > p.cap ? 8 : 4) + size_t(p.top + 3) / 4 * 16 + size_t(p.window) * 8;
+  const int rows = p.c1 - p.c0;
+  return rows > 8 * num_sms ? launch_choose_for<128>(p, smem, st)
+         : rows > num_sms   ? launch_choose_for<256>(p, smem, st)
+                            : launch_choose_for<1024>(p, smem, st);
+}
+
+// The workspace: keys of a chunk of rows, then the tiles of all chunks.  Sized for the call
+// with cu_q; one without it needs the keys alone.
+struct SelectLayout {
+  int64_t ld;
+  int32_t rows, chunks;  // of a chunk; how many
+  size_t tiles, tile_q, bytes;
+};
+
+SelectLayout select_layout(int32_t Tq, int32_t B, int32_t P, int32_t page_size, int32_t Hi, int32_t Di, int32_t block) {
+  SelectLayout l{};
+  l.ld = blocks_ld(P, page_size, block);
+  l.rows = chunk_rows(Tq, l.ld);
+  l.chunks = l.rows > 0 ? int32_t((int64_t(Tq) + l.rows - 1) / l.rows) : 0;
+  l.tiles = (size_t(l.rows) * size_t(l.ld) * 4 + 255) / 256 * 256;
+  l.tile_q = l.bytes = l.tiles;
+  if (l.ld > 0 && use_wide(Tq, B, Hi, true)) {
+    const size_t n = size_t(wide_max_tiles(l.rows, B, Hi)) * size_t(l.chunks);
+    l.tile_q = l.tiles + (n * sizeof(int4) + 255) / 256 * 256;
+    l.bytes = l.tile_q + n * wide_tile_bytes(Di);
+  }
+  return l;
+}
+
+qsa_status_t check_select_sizes(int32_t Tq, int32_t B, int32_t P, int32_t page_size, int32_t Hi, int32_t Di,
+                                int32_t block) {
   if (Tq < 0 || B < 0 || P < 0)
     QSA_REJECT(QSA_ERR_INVALID_ARG, "negative size: Tq=%d B=%d P=%d", Tq, B, P);
   if (block < 1 || block > kMaxBlock)
@@ -423,17 +1134,19 @@ qsa_status_t check_select_sizes(int32_t Tq, int32_t B, int32_t P, int32_t page_s
     QSA_REJECT(QSA_ERR_INVALID_ARG, "page_size=%d must be a positive multiple of block=%d", page_size, block);
   if (int64_t(P) * page_size > INT32_MAX - 4096)
     QSA_REJECT(QSA_ERR_UNSUPPORTED, "a page table of %lld tokens", (long long)(int64_t(P) * page_size));
+  if (Di != 64 && Di != 128) QSA_REJECT(QSA_ERR_UNSUPPORTED, "index dimension %d (64 or 128)", Di);
+  if (Hi < 1 || Hi > QSA_MAX_INDEX_HEADS)
+    QSA_REJECT(QSA_ERR_UNSUPPORTED, "%d index heads (1..%d)", Hi, QSA_MAX_INDEX_HEADS);
   return QSA_OK;
 }
 
 }  // namespace
 
-extern "C" size_t qsa_select_slots_workspace_bytes(int32_t Tq, int32_t B, int32_t P,
-                                                   int32_t page_size, int32_t block) {
+extern "C" size_t qsa_select_slots_workspace_bytes(int32_t Tq, int32_t B, int32_t P, int32_t page_size,
+                                                   int32_t Hi, int32_t Di, int32_t block) {
   set_error_detail("%s", "");
-  if (check_select_sizes(Tq, B, P, page_size, block) != QSA_OK) return SIZE_MAX;
-  const int64_t ld = blocks_ld(P, page_size, block);
-  return size_t(chunk_rows(Tq, ld)) * size_t(ld) * 4;
+  if (check_select_sizes(Tq, B, P, page_size, Hi, Di, block) != QSA_OK) return SIZE_MAX;
+  return select_layout(Tq, B, P, page_size, Hi, Di, block).bytes;
 }
 
 extern "C" qsa_status_t qsa_select_slots(
@@ -445,13 +1158,10 @@ extern "C" qsa_status_t qsa_select_slots(
     int64_t idx_stride_t, int32_t* width, void* workspace, size_t workspace_bytes,
     uint32_t* err_word, void* stream) {
   set_error_detail("%s", "");
-  const qsa_status_t sizes = check_select_sizes(Tq, B, P, page_size, block);
+  const qsa_status_t sizes = check_select_sizes(Tq, B, P, page_size, Hi, Di, block);
   if (sizes != QSA_OK) return sizes;
   if (pages < 0 || pages * page_size > INT32_MAX)
     QSA_REJECT(QSA_ERR_INVALID_ARG, "%lld pages of %d slots: slots are int32", (long long)pages, page_size);
-  if (Di != 64 && Di != 128) QSA_REJECT(QSA_ERR_UNSUPPORTED, "index dimension %d (64 or 128)", Di);
-  if (Hi < 1 || Hi > QSA_MAX_INDEX_HEADS)
-    QSA_REJECT(QSA_ERR_UNSUPPORTED, "%d index heads (1..%d)", Hi, QSA_MAX_INDEX_HEADS);
   if (top_blocks < 1 || int64_t(top_blocks) * block > QSA_MAX_TOP_BLOCKS)
     QSA_REJECT(QSA_ERR_INVALID_ARG, "top_blocks=%d of %d slots: 1..%d slots", top_blocks, block, QSA_MAX_TOP_BLOCKS);
   if (sink_blocks < 0 || local_blocks < 0 || int64_t(sink_blocks) + local_blocks > top_blocks)
@@ -471,9 +1181,11 @@ extern "C" qsa_status_t qsa_select_slots(
   if (!stride_multiple(q_stride_t, 2, 16) || !stride_multiple(q_stride_h, 2, 16) ||
       !stride_multiple(code_stride, 1, 16) || weight_stride < 0 || page_stride < 0 || idx_stride_t < 0)
     QSA_REJECT(QSA_ERR_INVALID_ARG, "strides must be non-negative, of q and codes multiples of 16 bytes");
-  const int64_t ld = blocks_ld(P, page_size, block);
-  const int32_t rows = chunk_rows(Tq, ld);
-  const size_t need = size_t(rows) * size_t(ld) * 4;
+  const SelectLayout lay = select_layout(Tq, B, P, page_size, Hi, Di, block);
+  const int64_t ld = lay.ld;
+  const int32_t rows = lay.rows;
+  const bool wide = use_wide(Tq, B, Hi, cu_q != nullptr);
+  const size_t need = cu_q != nullptr ? lay.bytes : lay.tiles;
   if (need > 0 && (workspace == nullptr || workspace_bytes < need))
     QSA_REJECT(QSA_ERR_WORKSPACE, "workspace of %zu bytes needed, got %zu", need,
                workspace == nullptr ? size_t(0) : workspace_bytes);
@@ -491,22 +1203,35 @@ extern "C" qsa_status_t qsa_select_slots(
   p.table = page_table, p.lens = seq_lens, p.cu = cu_q;
   p.out = slot_idx, p.width = width;
   p.keys = static_cast<uint32_t*>(workspace);
+  p.tiles = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + lay.tiles);
+  p.tile_q = static_cast<uint8_t*>(workspace) + lay.tile_q;
   p.err_word = err_word;
   p.q_st = q_stride_t, p.q_sh = q_stride_h, p.w_st = weight_stride, p.code_st = code_stride;
   p.table_st = page_stride, p.out_st = idx_stride_t, p.pages = pages, p.ld = ld;
   p.Tq = Tq, p.B = B, p.P = P, p.page_size = page_size, p.per_page = page_size / block;
   p.Hi = Hi, p.block = block, p.top = top_blocks, p.sink = sink_blocks, p.local = local_blocks;
   const auto st = static_cast<cudaStream_t>(stream);
-  const size_t list = size_t(top_blocks) * 4;
-  for (int64_t c0 = 0; c0 < Tq; c0 += rows) {
+  p.page_magic = uint32_t(((uint64_t(1) << 32) + p.per_page - 1) / p.per_page);
+  p.block_magic = uint32_t(((uint64_t(1) << 32) + block - 1) / block);
+  const bool scored = ld > top_blocks;  // (a table of at most top_blocks blocks needs no scores)
+  auto wide_launch = [&](int chunk) {
+    return Di == 128 ? launch_wide_for<128>(p, chunk, rows, lay.chunks, num_sms, st)
+                     : launch_wide_for<64>(p, chunk, rows, lay.chunks, num_sms, st);
+  };
+  if (scored && wide) {
+    if (lay.chunks > 65535) QSA_REJECT(QSA_ERR_UNSUPPORTED, "%d chunks of rows in one call", lay.chunks);
+    if ((e = wide_launch(-1)) != cudaSuccess) return launch_status(e, "qsa_select_slots: query codes");
+  }
+  for (int32_t chunk = 0; chunk < lay.chunks; ++chunk) {
+    const int64_t c0 = int64_t(chunk) * rows;
     p.c0 = int32_t(c0);
     p.c1 = int32_t(c0 + rows < Tq ? c0 + rows : Tq);
-    if (ld > top_blocks) {  // (a table of at most top_blocks blocks needs no scores)
-      e = Di == 128 ? launch_score_for<128>(p, num_sms, st) : launch_score_for<64>(p, num_sms, st);
+    if (scored) {
+      e = wide ? wide_launch(chunk)
+          : Di == 128 ? launch_score_for<128>(p, num_sms, st) : launch_score_for<64>(p, num_sms, st);
       if (e != cudaSuccess) return launch_status(e, "qsa_select_slots: score");
     }
-    qsa_select_choose_kernel<<<p.c1 - p.c0, kChooseThreads, list, st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return launch_status(e, "qsa_select_slots: choice");
+    if ((e = launch_choose(p, num_sms, st)) != cudaSuccess) return launch_status(e, "qsa_select_slots: choice");
   }
   return QSA_OK;
 }

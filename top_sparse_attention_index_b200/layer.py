@@ -173,9 +173,9 @@ def pack_index_keys(keys, blocks, codes, scales, block=4, err_word=None, stream=
     return codes, scales
 
 
-def qsa_select_slots_workspace_bytes(Tq, B, P, page_size, block) -> int:
+def qsa_select_slots_workspace_bytes(Tq, B, P, page_size, Hi, Di, block) -> int:
     """Workspace bytes of qsa_select_slots; raises QSAError for invalid sizes."""
-    n = int(load_library().qsa_select_slots_workspace_bytes(Tq, B, P, page_size, block))
+    n = int(load_library().qsa_select_slots_workspace_bytes(Tq, B, P, page_size, Hi, Di, block))
     if n == ctypes.c_size_t(-1).value:
         raise QSAError(1, qsa_last_error_detail())
     return n
@@ -216,7 +216,7 @@ def select_slots(q, weight, codes, scales, page_table, seq_lens, top_blocks, pag
         _check_err_word(err_word, device)
     if block < 1 or page_size < 1 or page_size % block:
         raise ValueError("page_size must be a positive multiple of block")
-    need = qsa_select_slots_workspace_bytes(Tq, B, P, page_size, block)
+    need = qsa_select_slots_workspace_bytes(Tq, B, P, page_size, Hi, Di, block)
     with _on(device, stream):
         if slot_idx is None:
             slot_idx = torch.empty(Tq, max(top_blocks, 0) * block + block - 1, dtype=torch.int32, device=device)
