@@ -279,7 +279,7 @@ constexpr int kWideCols = 256;
 constexpr int kWideStages = 6;                     // key tiles in shared memory
 constexpr int kWideQ = 3;                          // Q tiles in shared memory (one more than a producer's lag)
 constexpr int kWideLag = 2;                        // tiles a producer has in flight behind the one it issues
-constexpr int kEpilogueWarps = 8, kProducerWarps = 4;
+constexpr int kEpilogueWarps = 16, kProducerWarps = 4;
 constexpr int kWideThreads = 32 * (kEpilogueWarps + kProducerWarps + 1);
 
 __host__ __device__ constexpr int wide_tile_bytes(int DI) { return kWideCols * (DI + 4); }  // codes, then gains
@@ -589,9 +589,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     }
   } else {
     // ---- dots to keys --------------------------------------------------------------------------
-    const int quad = warp & 3, half = warp >> 2;  // lanes of the accumulator, half of its columns
+    constexpr int kParts = kEpilogueWarps / 4, kPartCols = kWideCols / kParts;
+    static_assert(kPartCols % 32 == 0, "whole loads");
+    const int quad = warp & 3, part = warp >> 2;  // lanes of the accumulator, part of its columns
     const int r = quad * 32 + lane;
-    constexpr int kHalfRows = kWideCols / 2 / HP;
+    constexpr int kPartRows = kPartCols / HP;
     int tile = tile0, kt = first_kt, qn = 0;
     int4 w = tiles[tile];
     for (int i = 0; i < share; ++i) {
@@ -610,18 +612,18 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const bool any_bad = __any_sync(0xffffffffu, !valid);
       const int j = kt * kKeyTile + r;
       const uint64_t scale2 = pack2(scale, scale);
-      const float* gains = reinterpret_cast<const float*>(sQ + (qn % kWideQ) * C::kQBytes + kWideCols * DI) + half * 128;
-      const int row0 = half * kHalfRows;
+      const float* gains = reinterpret_cast<const float*>(sQ + (qn % kWideQ) * C::kQBytes + kWideCols * DI) + part * kPartCols;
+      const int row0 = part * kPartRows;
       uint32_t* out = p.keys + int64_t(w.y + row0 - p.c0) * p.ld + j;
       const bool store = j < p.ld;
       const uint64_t minus = pack2(-8388608.f, -8388608.f), zero = pack2(0.f, 0.f);
       uint64_t sum = zero;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < kPartCols / 32; ++c) {
         uint32_t d[32];
-        tmem_ld32(d, tmem + acc * kWideCols + half * 128 + c * 32 + (uint32_t(quad * 32) << 16));
+        tmem_ld32(d, tmem + acc * kWideCols + part * kPartCols + c * 32 + (uint32_t(quad * 32) << 16));
         asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-        if (c == 3) {  // the accumulator has been read
+        if (c == kPartCols / 32 - 1) {  // the accumulator has been read
           asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kAccFree + acc));
@@ -674,7 +676,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 
 constexpr int kBins = 512;     // of a histogram: 16 per lane of one warp
 constexpr int kSample = 1024;  // keys that estimate the border of a long row
-constexpr int kBatch = 4;      // 16-byte loads of keys in flight per thread
+constexpr int kBatch = 2;      // 16-byte loads of keys per thread and step
 constexpr int kWindow = 1024;  // most words of the marks: 32,768 blocks at a time
 
 // The border of a row: blocks of a larger key are taken, of `equal` equal ones the first `want`.
@@ -690,9 +692,15 @@ struct ChooseShared {
   int n_few, bin, above, count, n;
 };
 
+// mask |= bit when key >= low: two instructions.
+__device__ __forceinline__ void keep_bit(uint32_t& mask, uint32_t key, uint32_t low, uint32_t bit) {
+  asm("{\n  .reg .pred q;\n  setp.ge.u32 q, %1, %2;\n  @q or.b32 %0, %0, %3;\n}\n" : "+r"(mask) : "r"(key), "r"(low), "r"(bit));
+}
+
 // The want-th largest (1 <= want <= n) of the keys key_at(0 .. n - 1), by histograms of the
 // key range that still holds it; the last step ranks at most 32 keys within each warp.
-template <int THREADS, class F>
+// Without EXACT: a key at most that one with few keys between them (`key` alone is meant).
+template <int THREADS, bool EXACT, class F>
 __device__ Border kth_largest(int n, int want, F key_at, ChooseShared& sh) {
   const int tid = threadIdx.x, lane = tid & 31;
   __syncthreads();  // (sh and the keys)
@@ -713,8 +721,11 @@ __device__ Border kth_largest(int n, int want, F key_at, ChooseShared& sh) {
     atomicMax(&sh.hi, hi);
   }
   __syncthreads();
-  lo = sh.lo;
+  const uint32_t least = sh.lo;
   hi = sh.hi;
+  // The keys are floats in order: most of a row's lie in a few octaves below the largest, so
+  // the first histogram takes four of them, and the whole range only if that is not enough.
+  lo = hi - least > (4u << 23) ? hi - (4u << 23) : least;
   for (;;) {
     const uint32_t range = hi - lo;
     const int shift = range < uint32_t(kBins) ? 0 : 32 - __clz(range) - 9;  // 2^9 = kBins
@@ -740,6 +751,7 @@ __device__ Border kth_largest(int n, int want, F key_at, ChooseShared& sh) {
         if (lane >= o) above += y;
       }
       above -= mine;
+      if (lane == 31 && above + mine < want) sh.bin = -1;
       if (above < want && above + mine >= want) {
 #pragma unroll
         for (int e = 15; e >= 0; --e) {
@@ -749,12 +761,19 @@ __device__ Border kth_largest(int n, int want, F key_at, ChooseShared& sh) {
       }
     }
     __syncthreads();
+    if (sh.bin < 0) {  // fewer keys than wanted above lo
+      lo = least;
+      for (int i = tid; i < kBins; i += THREADS) sh.hist[i] = 0;
+      __syncthreads();
+      continue;
+    }
     want -= sh.above;
     const int count = sh.count;
     lo += uint32_t(sh.bin) << shift;
     hi = lo + min(hi - lo, (1u << shift) - 1u);
     if (shift == 0) return {lo, want, count};
     if (count <= 32) {
+      if (!EXACT) return {lo, want, count};
 #pragma unroll 4
       for (int i = tid; i < n; i += THREADS) {
         const uint32_t k = key_at(i);
@@ -788,7 +807,7 @@ __device__ Border kth_largest(int n, int want, F key_at, ChooseShared& sh) {
 // (radix passes over the whole row, four reads and a conflicting shared-memory atomic per key
 // and pass, took 165 us per 1,024 rows of 15,500 blocks).
 template <int THREADS>
-__global__ void __launch_bounds__(THREADS) qsa_select_choose_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : 1) qsa_select_choose_kernel(const SelectParams p) {
   extern __shared__ __align__(16) uint32_t dyn[];
   uint32_t* sKey = dyn;                                       // [cap]
   int* sIdx = reinterpret_cast<int*>(sKey + p.cap);           // [cap], absent when every row fits
@@ -831,13 +850,18 @@ __global__ void __launch_bounds__(THREADS) qsa_select_choose_kernel(const Select
   if (f <= p.top) {
     for (int j = tid; j < f; j += THREADS) sList[j] = first_slot(j);
   } else {
-    auto forced = [&](int j, uint32_t k) { return (j < p.sink || j >= f - p.local) ? 0xffffffffu : k; };
-    auto in_row = [&](int j) { return forced(j, __ldg(row + j)); };
+    // blocks that are taken whatever they score do not take part in the search
+    const int want = p.top - p.sink - p.local;
+    auto forced = [&](int j) { return j < p.sink || j >= f - p.local; };
+    auto searched = [&](int j, uint32_t k) { return forced(j) ? 0u : k; };
+    auto in_row = [&](int j) { return searched(j, __ldg(row + j)); };
     const uint4* row4 = reinterpret_cast<const uint4*>(row);  // (ld is a multiple of 32)
     auto in_list = [&](int i) { return sKey[i]; };
-    Border border;
-    int listed = -1;  // keys collected with their blocks; -1: every block of the row is searched
-    if (f <= p.cap) {
+    Border border{0xffffffffu, 0, 0};
+    int listed = want > 0 ? -1 : 0;  // keys collected with their blocks; -1: every block of the row is searched
+    if (want == 0) {
+      // nothing but those
+    } else if (f <= p.cap) {
       for (int i0 = tid; i0 * 4 < f; i0 += THREADS * kBatch) {
         uint4 k[kBatch];
 #pragma unroll
@@ -847,11 +871,11 @@ __global__ void __launch_bounds__(THREADS) qsa_select_choose_kernel(const Select
         for (int u = 0; u < kBatch; ++u) {
           const int j = (i0 + u * THREADS) * 4;
           if (j >= f) break;
-          *reinterpret_cast<uint4*>(sKey + j) = make_uint4(forced(j, k[u].x), forced(j + 1, k[u].y),
-                                                           forced(j + 2, k[u].z), forced(j + 3, k[u].w));
+          *reinterpret_cast<uint4*>(sKey + j) = make_uint4(searched(j, k[u].x), searched(j + 1, k[u].y),
+                                                           searched(j + 2, k[u].z), searched(j + 3, k[u].w));
         }
       }
-      border = kth_largest<THREADS>(f, p.top, in_list, sh);
+      border = kth_largest<THREADS, true>(f, want, in_list, sh);
     } else {
       {
         uint32_t k[kSample / THREADS];  // one from each of kSample equal parts of the row
@@ -863,52 +887,72 @@ __global__ void __launch_bounds__(THREADS) qsa_select_choose_kernel(const Select
 #pragma unroll
         for (int u = 0; u < kSample / THREADS; ++u) sKey[tid + u * THREADS] = k[u];
       }
-      // of the row's `top` best, about `hits` are in the sample: the border lies 5 deviations lower
-      const float hits = float(p.top) * kSample / float(f);
-      const uint32_t low =
-          kth_largest<THREADS>(kSample, min(int(hits + 5.f * sqrtf(hits)) + 6, kSample), in_list, sh).key;
-      __syncthreads();
-      if (tid == 0) sh.n = 0;
-      __syncthreads();
-      const uint32_t below = (1u << lane) - 1u;
-      for (int i0 = warp * 32; i0 * 4 < f; i0 += THREADS * kBatch) {
-        uint4 raw[kBatch];
+      // of the row's `want` best, about `hits` are in the sample: the border lies 4 deviations lower
+      const float hits = float(want) * kSample / float(f);
+      int rank = min(int(hits + 4.f * sqrtf(hits)) + 4, kSample);
+      uint32_t low = kth_largest<THREADS, false>(kSample, rank, in_list, sh).key;
+      // The blocks of keys from `low` up.  More than there is room for: the want-th largest of
+      // those that had room is a better border, since as many keys as wanted reach it.  Fewer
+      // than wanted, or no better border: every block of the row is searched.
+      for (int tries = 0; tries < 3; ++tries) {
+        __syncthreads();
+        if (tid == 0) sh.n = 0;
+        __syncthreads();
+        uint4 raw[kBatch], next[kBatch];
+        auto load = [&](int i0) {
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          raw[u] = make_uint4(0u, 0u, 0u, 0u);
-          if ((i0 + lane + u * THREADS) * 4 < f) raw[u] = __ldg(row4 + i0 + lane + u * THREADS);
-        }
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          const int j = (i0 + lane + u * THREADS) * 4;
-          const uint32_t k[4] = {forced(j, raw[u].x), forced(j + 1, raw[u].y), forced(j + 2, raw[u].z),
-                                 forced(j + 3, raw[u].w)};
-          uint32_t keep[4];
-          int total = 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            keep[e] = __ballot_sync(0xffffffffu, j + e < f && k[e] >= low);
-            total += __popc(keep[e]);
+          for (int u = 0; u < kBatch; ++u) {
+            next[u] = make_uint4(0u, 0u, 0u, 0u);
+            if ((i0 + lane + u * THREADS) * 4 < f) next[u] = __ldg(row4 + i0 + lane + u * THREADS);
           }
-          if (total == 0) continue;
-          int at = 0;
-          if (lane == 0) at = atomicAdd(&sh.n, total);
-          at = __shfl_sync(0xffffffffu, at, 0);
+        };
+        load(warp * 32);
+        for (int i0 = warp * 32; i0 * 4 < f; i0 += THREADS * kBatch) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int i = at + __popc(keep[e] & below);
-            if (((keep[e] >> lane) & 1) && i < p.cap) sKey[i] = k[e], sIdx[i] = j + e;
-            at += __popc(keep[e]);
+          for (int u = 0; u < kBatch; ++u) raw[u] = next[u];
+          load(i0 + THREADS * kBatch);
+          uint32_t k[4 * kBatch], keep = 0u;  // a bit per key of this lane
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u)
+            k[4 * u] = raw[u].x, k[4 * u + 1] = raw[u].y, k[4 * u + 2] = raw[u].z, k[4 * u + 3] = raw[u].w;
+          if (i0 * 4 >= p.sink && (i0 + 32 + (kBatch - 1) * THREADS) * 4 <= f - p.local) {
+#pragma unroll
+            for (int x = 0; x < 4 * kBatch; ++x) keep_bit(keep, k[x], low, 1u << x);
+          } else {
+#pragma unroll
+            for (int x = 0; x < 4 * kBatch; ++x) {
+              const int j = (i0 + lane + (x >> 2) * THREADS) * 4 + (x & 3);
+              keep |= j < f && !forced(j) && k[x] >= low ? 1u << x : 0u;
+            }
+          }
+          const int mine = __popc(keep);
+          int at = mine;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, at, o);
+            if (lane >= o) at += y;
+          }
+          int before = 0;
+          if (lane == 31 && at > 0) before = atomicAdd(&sh.n, at);
+          at += __shfl_sync(0xffffffffu, before, 31) - mine;
+          while (keep != 0u) {
+            const int x = __ffs(keep) - 1;
+            keep &= keep - 1;
+            if (at < p.cap) sIdx[at] = (i0 + lane + (x >> 2) * THREADS) * 4 + (x & 3);
+            ++at;
           }
         }
+        __syncthreads();
+        const int n = sh.n, room = min(n, p.cap);
+        if (n < want) break;
+#pragma unroll 4
+        for (int i = tid; i < room; i += THREADS) sKey[i] = __ldg(row + sIdx[i]);
+        border = kth_largest<THREADS, true>(room, want, in_list, sh);
+        if (n == room) listed = n;
+        if (n == room || border.key == low) break;
+        low = border.key;
       }
-      __syncthreads();
-      if (sh.n >= p.top && sh.n <= p.cap) {
-        listed = sh.n;
-        border = kth_largest<THREADS>(listed, p.top, in_list, sh);
-      } else {
-        border = kth_largest<THREADS>(f, p.top, in_row, sh);
-      }
+      if (listed < 0) border = kth_largest<THREADS, true>(f, want, in_row, sh);
     }
     // ---- marks and places, a window of blocks at a time ----------------------------------------
     const bool all_same = border.want == border.equal;  // no choice between equal keys
@@ -925,13 +969,17 @@ __global__ void __launch_bounds__(THREADS) qsa_select_choose_kernel(const Select
           const int j = sIdx[i], w = (j >> 5) - w0;
           if (k >= border.key && w >= 0 && w < words) atomicOr(over(k) ? &sOver[w] : &sSame[w], 1u << (j & 31));
         }
+        for (int i = tid; i < p.sink + p.local; i += THREADS) {
+          const int j = i < p.sink ? i : f - p.local + (i - p.sink), w = (j >> 5) - w0;
+          if (w >= 0 && w < words) atomicOr(&sOver[w], 1u << (j & 31));
+        }
       } else {
         __syncthreads();
         for (int w = warp; w < words; w += THREADS / 32) {
           const int j = (w0 + w) * 32 + lane;
           const uint32_t k = j < f ? (f <= p.cap ? sKey[j] : in_row(j)) : 0u;
-          const uint32_t o = __ballot_sync(0xffffffffu, j < f && over(k));
-          const uint32_t s = __ballot_sync(0xffffffffu, j < f && !all_same && k == border.key);
+          const uint32_t o = __ballot_sync(0xffffffffu, j < f && (over(k) || forced(j)));
+          const uint32_t s = __ballot_sync(0xffffffffu, j < f && !all_same && k == border.key && !forced(j));
           if (lane == 0) sOver[w] = o, sSame[w] = s;
         }
       }
@@ -952,28 +1000,34 @@ __global__ void __launch_bounds__(THREADS) qsa_select_choose_kernel(const Select
           any &= any - 1;
           const bool is_over = (o >> bit) & 1;
           if (is_over || before_same < border.want)
-            sList[before + (all_same ? 0 : min(before_same, border.want))] = first_slot((w0 + w) * 32 + bit);
+            sList[before + (all_same ? 0 : min(before_same, border.want))] = (w0 + w) * 32 + bit;
           if (is_over) ++before; else ++before_same;
         }
       }
       have += total;
       same += total_same;
     }
+    __syncthreads();
+    for (int i = tid; i < p.top; i += THREADS) sList[i] = first_slot(sList[i]);
   }
   __syncthreads();
   int32_t* out = p.out + t * p.out_st;
   const int W = p.top * p.block + p.block - 1, full = taken * p.block, tail = seen - f * p.block;
-  const int tail_slot = tail > 0 ? first_slot(f) : -1;
-  for (int w = tid; w < W; w += THREADS) {
-    int s = -1;
-    if (w < full) {
-      const int i = p.block == 1 ? w : int(__umulhi(uint32_t(w), p.block_magic));  // w / block (w below 2^14)
-      s = sList[i] < 0 ? -1 : sList[i] + (w - i * p.block);
-    } else if (w < full + tail) {
-      s = tail_slot < 0 ? -1 : tail_slot + (w - full);
+  if (p.block == 4) {  // (the usual micro-block: no division)
+#pragma unroll 4
+    for (int w = tid; w < full; w += THREADS) {
+      const int s = sList[w >> 2];
+      out[w] = s < 0 ? -1 : s + (w & 3);
     }
-    out[w] = s;
+  } else {
+    for (int w = tid; w < full; w += THREADS) {
+      const int i = p.block == 1 ? w : int(__umulhi(uint32_t(w), p.block_magic));  // w / block (w below 2^14)
+      out[w] = sList[i] < 0 ? -1 : sList[i] + (w - i * p.block);
+    }
   }
+  const int tail_slot = tail > 0 ? first_slot(f) : -1;
+  for (int w = full + tid; w < W; w += THREADS)
+    out[w] = w < full + tail && tail_slot >= 0 ? tail_slot + (w - full) : -1;
   if (tid == 0) p.width[t] = full + tail;
 }
 
@@ -1018,9 +1072,10 @@ int heads_padded(int Hi) {
   return hp;
 }
 
-// The tcgen05 form pays once a tile's 256 columns are filled to a quarter on average.
+// The tcgen05 form (a pair of rows within 64 columns: at most 32 heads) pays once a tile's 256
+// columns are filled to a quarter on average.
 bool use_wide(int32_t Tq, int32_t B, int32_t Hi, bool has_cu) {
-  return has_cu && int64_t(Tq) * heads_padded(Hi) * 4 >= int64_t(B) * kWideCols;
+  return has_cu && Hi <= 32 && int64_t(Tq) * heads_padded(Hi) * 4 >= int64_t(B) * kWideCols;
 }
 
 int64_t wide_max_tiles(int32_t rows, int32_t B, int32_t Hi) {  // a sequence adds at most one partial tile
@@ -1059,7 +1114,6 @@ cudaError_t launch_wide_for(const SelectParams& p, int chunk, int chunk_rows, in
     QSA_WIDE(8)
     QSA_WIDE(16)
     QSA_WIDE(32)
-    QSA_WIDE(64)
     default: return cudaErrorInvalidValue;
   }
 #undef QSA_WIDE
@@ -1096,7 +1150,7 @@ cudaError_t launch_choose(SelectParams& p, int num_sms, cudaStream_t st) {
   p.window = p.ld / 32 < kWindow ? int(p.ld / 32) : kWindow;  // (ld is a multiple of 32)
   const size_t smem = size_t(p.cap) * (p.ld > p.cap ? 8 : 4) + size_t(p.top + 3) / 4 * 16 + size_t(p.window) * 8;
   const int rows = p.c1 - p.c0;
-  return rows > 8 * num_sms ? launch_choose_for<128>(p, smem, st)
+  return rows > 2 * num_sms ? launch_choose_for<128>(p, smem, st)
          : rows > num_sms   ? launch_choose_for<256>(p, smem, st)
                             : launch_choose_for<1024>(p, smem, st);
 }
