@@ -1,9 +1,10 @@
-"""Build libqsa.so (the C-ABI CUDA library) in-tree with nvcc for sm_100a.
+"""Build libqsa.so (the C-ABI CUDA library) in-tree with nvcc for sm_100a, and _layer_ext.so
+(the layer operators' torch-facing calls, host code only) with g++.
 
     python -m top_sparse_attention_index_b200.build_lib [--force] [--verbose-ptxas]
 
 The library links the CUDA runtime statically, so the only run-time dependency is the
-NVIDIA driver.
+NVIDIA driver.  The extension links against the installed torch and libqsa.so beside it.
 """
 from __future__ import annotations
 
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
@@ -18,6 +20,8 @@ ROOT = PKG.parent
 CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 LIBRARY = PKG / "libqsa.so"
+EXTENSION = PKG / "_layer_ext.so"
+EXT_SOURCE = CSRC / "qsa_torch.cpp"
 SOURCES = [CSRC / "qsa_api.cu", CSRC / "qsa_attn.cu", CSRC / "qsa_noalloc.cu", CSRC / "qsa_probe.cu",
            CSRC / "qsa_probe_mma.cu", CSRC / "qsa_peer.cu",
            CSRC / "qsa_rope.cu", CSRC / "qsa_select.cu", CSRC / "qsa_decode.cu"]
@@ -41,16 +45,41 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libqsa.so")
 
 
+def _stale(output: Path, depends) -> bool:
+    return not output.exists() or output.stat().st_mtime < max(p.stat().st_mtime for p in depends)
+
+
+def build_extension(force: bool = False) -> Path:
+    """_layer_ext.so; libqsa.so has to be there."""
+    if not force and not _stale(EXTENSION, [EXT_SOURCE, INCLUDE / "qsa_layer.h", INCLUDE / "qsa.h"]):
+        return EXTENSION
+    import torch
+    root = Path(torch.__file__).resolve().parent
+    cuda = Path(nvcc()).resolve().parent.parent
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", str(INCLUDE), "-isystem", str(root / "include"),
+           "-isystem", str(root / "include/torch/csrc/api/include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", str(cuda / "include"),
+           str(EXT_SOURCE), "-o", str(EXTENSION), "-L", str(PKG), "-l:libqsa.so", "-Wl,-rpath,$ORIGIN",
+           "-L", str(root / "lib"), "-ltorch_python", "-ltorch", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    subprocess.run(cmd, check=True)
+    return EXTENSION
+
+
 def build(force: bool = False, verbose_ptxas: bool = False, output: Path = LIBRARY) -> Path:
     output = Path(output)
-    if (not force and output.exists()
-            and output.stat().st_mtime >= max(p.stat().st_mtime for p in DEPENDS)):
+    if not force and not _stale(output, DEPENDS):
+        if output == LIBRARY:
+            build_extension()
         return output
     cmd = [nvcc(), *NVCC_FLAGS, "-I", str(INCLUDE), "-I", str(CSRC)]
     if verbose_ptxas:
         cmd += ["-Xptxas", "-v"]
     cmd += [str(s) for s in SOURCES] + ["-o", str(output)]
     subprocess.run(cmd, check=True)
+    if output == LIBRARY:
+        build_extension(force)
     return output
 
 
