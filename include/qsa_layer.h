@@ -154,8 +154,8 @@ qsa_status_t qsa_select_slots(const void* q, int64_t q_stride_t, int64_t q_strid
  * tokens i whose slots the page table names (slot = page_table[b, i / page_size] * page_size
  * + i mod page_size):
  *   s_i = scale * q[b, h] . k_cache[slot_i, j];   out[b, h] = sum_i softmax(s)_i v_cache[slot_i, j]
- * or exactly +0 when the sequence has no token.  The length is split over thread blocks,
- * whose partial results are joined by their log-sum-exp.
+ * or exactly +0 when the sequence has no token.  The tokens of all sequences are shared out
+ * evenly over the thread blocks; pieces of one sequence are joined by their log-sum-exp.
  *
  *   q            bf16 [B, Hq, D], strides (b, h);  out bf16 [B, Hq, D].
  *   k_cache, v_cache   [pages * page_size, Hkv, D]: bf16, or E4M3 codes with kv_fp8
@@ -166,15 +166,16 @@ qsa_status_t qsa_select_slots(const void* q, int64_t q_stride_t, int64_t q_strid
  *                QSA_ERRBIT_WIDTH_RANGE.
  *   lse          float [B, Hq] (contiguous), or NULL: the base-2 log-sum-exp of the scaled
  *                scores (-infinity without a token).
- *   nsplit       0 = automatic, else the number of splits of the length P * page_size
- *                (adjusted as the plan does).
+ *   blocks       0 = automatic, else the number of thread blocks, at most 65536 (the plan makes it
+ *                a multiple of Hkv, and smaller when there is less work); the order of the
+ *                sums, and with it the last bits, depend on it.
  *   workspace    as planned, 16-byte aligned (fp32 partial outputs and log-sum-exp).
  *   D must be 256 and 1 <= Hq / Hkv <= 16.  With kv_fp8 the products run on 16-bit floats:
  *   a query element of 65536 or more sets QSA_ERRBIT_Q_RANGE (that row is not valid).
  */
 int32_t qsa_paged_decode_plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t P,
-                              int32_t page_size, int32_t num_sms, int32_t nsplit_request,
-                              size_t* workspace_bytes);
+                              int32_t page_size, int32_t kv_fp8, int32_t num_sms,
+                              int32_t blocks_request, size_t* workspace_bytes);
 qsa_status_t qsa_paged_decode(const void* q, int64_t q_stride_b, int64_t q_stride_h,
                               const void* k_cache, int64_t k_stride_s, int64_t k_stride_h,
                               const void* v_cache, int64_t v_stride_s, int64_t v_stride_h,
@@ -183,7 +184,7 @@ qsa_status_t qsa_paged_decode(const void* q, int64_t q_stride_b, int64_t q_strid
                               int32_t D, int32_t P, int64_t pages, int32_t page_size, float scale,
                               int32_t kv_fp8, float k_scale, float v_scale, void* out,
                               int64_t out_stride_b, int64_t out_stride_h, float* lse,
-                              int32_t nsplit, void* workspace, size_t workspace_bytes,
+                              int32_t blocks, void* workspace, size_t workspace_bytes,
                               uint32_t* err_word, void* stream);
 
 #ifdef __cplusplus

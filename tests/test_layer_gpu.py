@@ -386,9 +386,9 @@ def test_decode_heads(Hq, Hkv, fp8):
 
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("page", [1, 3, 16, 24, 100, 256])
-@pytest.mark.parametrize("nsplit", [0, 1, 3, 50])
-def test_decode_pages_and_splits(page, nsplit, fp8):
-    check_decode(decode_case(51, [999, 15, 17, 128, 0, 500], 12, 2, page, fp8), nsplit=nsplit)
+@pytest.mark.parametrize("blocks", [0, 1, 3, 50])
+def test_decode_pages_and_splits(page, blocks, fp8):
+    check_decode(decode_case(51, [999, 15, 17, 128, 0, 500], 12, 2, page, fp8), blocks=blocks)
 
 
 @pytest.mark.parametrize("n", [0, 1, 2, 15, 16, 17, 31, 32, 33, 47, 63, 64, 65, 127, 129])
@@ -428,7 +428,7 @@ def test_decode_pages_outside_the_pool_are_masked():
         c["page_table"][0, 2], c["page_table"][0, 18], c["page_table"][1, :] = -1, 10 ** 9, -2 ** 31
         err, out = check_decode(c)
         assert err == SLOT_RANGE and (out[1] == 0).all()
-        check_decode(c, nsplit=5)
+        check_decode(c, blocks=5)
 
 
 def test_decode_ignores_rows_behind_the_end():

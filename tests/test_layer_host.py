@@ -98,16 +98,16 @@ def test_select_refusals(lib, change, status):
     assert (qsa.qsa_last_error_detail() != "") == (status != 0)
 
 
-DECODE = ("q qb qh k ks kh v vs vh table ts lens B Hq Hkv D P pages page scale fp8 ksc vsc out ob oh lse nsplit work "
+DECODE = ("q qb qh k ks kh v vs vh table ts lens B Hq Hkv D P pages page scale fp8 ksc vsc out ob oh lse blocks work "
           "bytes err stream")
 DECODE_OK = dict(q=A, qb=4096, qh=256, k=A, ks=512, kh=256, v=A, vs=512, vh=256, table=A, ts=16, lens=A, B=0, Hq=16,
                  Hkv=2, D=256, P=16, pages=40, page=64, scale=0.0625, fp8=0, ksc=1.0, vsc=1.0, out=A, ob=4096, oh=256,
-                 lse=None, nsplit=4, work=A, bytes=1 << 30, err=None, stream=None)
+                 lse=None, blocks=4, work=A, bytes=1 << 30, err=None, stream=None)
 
 
 @pytest.mark.parametrize("change,status", [
     (dict(), 0), (dict(B=-1), 1), (dict(P=-1), 1), (dict(Hq=15), 1), (dict(Hkv=0), 1), (dict(D=128), 2),
-    (dict(Hq=34), 2), (dict(page=0), 1), (dict(page=1 << 28), 2), (dict(nsplit=-1), 1), (dict(fp8=2), 1),
+    (dict(Hq=34), 2), (dict(page=0), 1), (dict(page=1 << 28), 2), (dict(blocks=-1), 1), (dict(blocks=65537), 1), (dict(fp8=2), 1),
     (dict(scale=math.nan), 1), (dict(fp8=1, ksc=math.inf), 1), (dict(pages=-1), 1),
     (dict(B=4, q=None), 1), (dict(B=4, k=None), 1), (dict(B=4, v=None), 1), (dict(B=4, table=None), 1),
     (dict(B=4, lens=None), 1), (dict(B=4, out=None), 1), (dict(B=4, q=A + 8), 1), (dict(B=4, k=A + 4), 1),
@@ -121,14 +121,18 @@ def test_decode_refusals(lib, change, status):
 
 @pytest.mark.parametrize("B,Hq,Hkv,P,page", [(1, 16, 2, 1, 64), (64, 24, 2, 128, 64), (1, 3, 1, 262144, 1),
                                              (4, 16, 2, 4096, 64), (300, 12, 1, 33, 100), (2, 16, 16, 0, 16)])
-@pytest.mark.parametrize("request_", [0, 1, 3, 1000000])
-def test_decode_plan(B, Hq, Hkv, P, page, request_):
-    n, ws = qsa.qsa_paged_decode_plan(B, Hq, Hkv, 256, P, page, 148, request_)
-    cap = P * page
-    assert 1 <= n <= max(1, -(-cap // 16))
-    assert ws == 0 if n == 1 else ws >= B * Hq * n * 257 * 4
+@pytest.mark.parametrize("request_", [0, 1, 3, 65536])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_decode_plan(B, Hq, Hkv, P, page, request_, fp8):
+    n, ws = qsa.qsa_paged_decode_plan(B, Hq, Hkv, 256, P, page, fp8, 148, request_)
+    # a block per KV head in every group; no group without two units of 32 tokens at the
+    # sequences' greatest length
+    assert n % Hkv == 0 and Hkv <= n <= Hkv * max(1, -(-B * -(-P * page // 32) // 2))
+    if request_:
+        assert n <= max(request_, Hkv)
+    assert ws == 0 if n == Hkv else ws >= n * 2 * (Hq // Hkv) * 257 * 4
     # a plan asked for again by its own count is itself (a caller sizes its workspace with it)
-    assert qsa.qsa_paged_decode_plan(B, Hq, Hkv, 256, P, page, 148, n) == (n, ws)
+    assert qsa.qsa_paged_decode_plan(B, Hq, Hkv, 256, P, page, fp8, 148, n) == (n, ws)
 
 
 def test_select_workspace_is_bounded():

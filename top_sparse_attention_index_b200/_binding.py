@@ -75,7 +75,7 @@ SIGNATURES = {
     "qsa_select_slots": (_i32, [_p, _i64, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _p, _p, _i32,
                                 _i32, _i32, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _p,
                                 _i64, _p, _p, _sz, _p, _p]),
-    "qsa_paged_decode_plan": (_i32, [_i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+    "qsa_paged_decode_plan": (_i32, [_i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
                                      ctypes.POINTER(_sz)]),
     "qsa_paged_decode": (_i32, [_p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _p, _i32,
                                 _i32, _i32, _i32, _i32, _i64, _i32, _f, _i32, _f, _f, _p, _i64,

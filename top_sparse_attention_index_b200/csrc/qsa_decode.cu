@@ -11,8 +11,8 @@ constexpr int kDecodeWarps = 2;
 constexpr int kDecodeThreads = 32 * kDecodeWarps;
 constexpr int kStages = 2;
 constexpr int kSub = 16;                 // slots of a warp's sub-tile (the M of one MMA)
-constexpr int kMinSplit = 64;            // slots: what a thread block has in flight at once
-constexpr int kJoinThreads = 256;
+constexpr int kUnit = kSub * kDecodeWarps;  // slots that the work is shared out in
+constexpr int kMinUnits = 2;                // of a thread block: what it has in flight at once
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kRescaleLog2 = 8.0f;
 
@@ -21,11 +21,12 @@ struct DecodeParams {
   const uint8_t *k, *v;
   const int32_t *table, *lens;
   uint16_t* out;
-  float *lse, *ws_o, *ws_lse;  // ws_o [B, Hq, nsplit, D], ws_lse [B, Hq, nsplit]
+  float *lse, *ws_o, *ws_lse;  // ws_o [blocks, 2, G, D], ws_lse [blocks, 2, G]
   uint32_t* err_word;
   int64_t q_sb, q_sh, o_sb, o_sh, table_st, pages;
   int64_t k_ss, k_sh, v_ss, v_sh;  // bytes
-  int32_t B, Hq, Hkv, G, P, page_size, nsplit, split_len;
+  int32_t B, Hq, Hkv, G, P, page_size;
+  uint32_t page_magic;  // 2^32 / page_size, rounded up
   float scale_log2, v_scale;
 };
 
@@ -34,6 +35,51 @@ __device__ __forceinline__ int tokens_of(const DecodeParams& p, int b, bool repo
   const int n = p.lens[b];
   if (report && p.err_word != nullptr && (n < 0 || n > most)) atomicOr(p.err_word, QSA_ERRBIT_WIDTH_RANGE);
   return int(min(int64_t(max(n, 0)), most));
+}
+
+__device__ __forceinline__ int units_of(int len) { return (len + kUnit - 1) / kUnit; }
+
+// The work: the units of all sequences in order, cut into `groups` shares whose sizes differ
+// by one at most.  Group c's Hkv thread blocks take the same share of one KV head each, side
+// by side in time: the heads' rows of a slot are neighbours in memory.
+struct Share {
+  int64_t each, longer;  // units of a share; the first `longer` shares have one more
+  int32_t groups;        // shares that hold units
+  __device__ int64_t begin(int64_t c) const { return c * each + (c < longer ? c : longer); }
+  __device__ int32_t owner(int64_t unit) const {  // the share that has this unit
+    const int64_t in_longer = longer * (each + 1);
+    return int32_t(unit < in_longer ? quotient(unit, each + 1) : longer + quotient(unit - in_longer, each));
+  }
+  static __device__ int64_t quotient(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
+  }
+};
+
+__device__ __forceinline__ Share share_of(int64_t total, int groups) {
+  const int64_t most = (total + kMinUnits - 1) / kMinUnits;
+  Share s{0, 0, int32_t(most < groups ? most : groups)};
+  if (s.groups > 0) {
+    s.each = Share::quotient(total, s.groups);
+    s.longer = total - s.each * s.groups;
+  }
+  return s;
+}
+
+// Units of all sequences and of those before sequence `b`; by every warp for itself.
+__device__ __forceinline__ int64_t units_before(const DecodeParams& p, int b, int64_t& all, bool report) {
+  int64_t mine = 0, before = 0;
+  for (int i = threadIdx.x & 31; i < p.B; i += 32) {
+    const int n = units_of(tokens_of(p, i, report));
+    mine += n;
+    before += i < b ? n : 0;
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    mine += __shfl_xor_sync(0xffffffffu, mine, d);
+    before += __shfl_xor_sync(0xffffffffu, before, d);
+  }
+  all = mine;
+  return before;
 }
 
 // NT n8 tiles hold the G heads of a KV head.  Rows in shared memory are padded by 16 bytes,
@@ -49,16 +95,22 @@ struct Decode {
   static constexpr int kMergePitch = kD + 4;
   static constexpr size_t kSmem = kRing + kQBytes;
   static constexpr int kMergeBytes = kDecodeWarps * NT * 8 * kMergePitch * 4;
+  // thread blocks of an SM: 228 KB of shared memory, 1 KB of each block reserved
+  static constexpr int kResident = (228 * 1024) / (int(kSmem) + 1024 + 512);
   static_assert(kMergeBytes <= int(kSmem), "the merge buffer reuses the ring and the Q rows");
 };
 
-// One thread block per (sequence, KV head, split of the length).  Each warp takes every
-// second 16-slot sub-tile of the split and runs a pipeline of its own: one bulk copy per K
-// or V row and lane, an mbarrier per stage, no block-wide barrier in the loop.  Scores are
-// S^T = K Q^T with the slots as M and the heads as N, so the group shares every row that is
-// read; the softmax is online (base 2, the reference moves only when the maximum rises by
-// more than 2^8); P is rounded to 16 bits for O^T += V^T P^T, and the denominator sums the
-// same rounded values.  The bound is HBM: every row is read once.
+// The units of all sequences are shared out evenly over the thread blocks that the device
+// holds at once, whatever the lengths (split evenly by the page table's capacity, 64 ragged
+// sequences took 157 us, so 113); a sequence that one block holds whole is written to the
+// output, a piece of one to the block's record (its first piece to record 0, its last to
+// record 1: pieces between them are whole sequences).
+// Within a block each warp takes every second 16-slot sub-tile and runs a pipeline of its
+// own: one bulk copy per K or V row and lane, an mbarrier per stage, no block-wide barrier in
+// the loop.  Scores are S^T = K Q^T with the slots as M and the heads as N, so the group
+// shares every row that is read; the softmax is online (base 2, the reference moves only when
+// the maximum rises by more than 2^8); P is rounded to 16 bits for O^T += V^T P^T, and the
+// denominator sums the same rounded values.  The bound is HBM: every row is read once.
 template <bool FP8, int NT>
 __global__ void __launch_bounds__(kDecodeThreads) qsa_paged_decode_kernel(const DecodeParams p) {
   using C = Decode<FP8, NT>;
@@ -67,32 +119,62 @@ __global__ void __launch_bounds__(kDecodeThreads) qsa_paged_decode_kernel(const 
   __shared__ float2 sState[kDecodeWarps][NT * 8];  // (m, l) of each warp and head
   uint8_t* sQ = smem + C::kRing;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int split = blockIdx.x % p.nsplit;
-  const int j = (blockIdx.x / p.nsplit) % p.Hkv, b = blockIdx.x / p.nsplit / p.Hkv;
-  const int len = tokens_of(p, b, tid == 0);
-  const int s0 = split * p.split_len, s1 = s0 + min(p.split_len, len - s0);  // (s0 is below the table's tokens)
-  const int h0 = j * p.G;
-  if (s0 >= s1) {  // nothing here; the only split of an empty sequence writes its zeros
-    if (p.nsplit == 1) {
-      for (int i = tid; i < p.G * (kD / 8); i += kDecodeThreads)
-        *reinterpret_cast<uint4*>(p.out + b * p.o_sb + (h0 + i / (kD / 8)) * p.o_sh + (i % (kD / 8)) * 8) =
-            make_uint4(0u, 0u, 0u, 0u);
-      if (p.lse != nullptr)
-        for (int g = tid; g < p.G; g += kDecodeThreads) p.lse[int64_t(b) * p.Hq + h0 + g] = kNegInf;
-    }
-    return;
-  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the join waits for this grid's end)
   if (tid == 0) {
     for (int i = 0; i < kDecodeWarps * kStages; ++i) mbar_init(smem_addr(sBar + i), 1);
     mbar_init_fence();
   }
-  __syncthreads();
+  int64_t total;
+  units_before(p, 0, total, blockIdx.x == 0 && warp == 0);
+  __syncthreads();  // the mbarriers
+  // sequences without a token: zeros
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    if (tokens_of(p, b, false) > 0) continue;
+    for (int i = tid; i < p.Hq * (kD / 8); i += kDecodeThreads)
+      *reinterpret_cast<uint4*>(p.out + b * p.o_sb + (i / (kD / 8)) * p.o_sh + (i % (kD / 8)) * 8) =
+          make_uint4(0u, 0u, 0u, 0u);
+    if (p.lse != nullptr)
+      for (int h = tid; h < p.Hq; h += kDecodeThreads) p.lse[int64_t(b) * p.Hq + h] = kNegInf;
+  }
+  const int groups = int(gridDim.x) / p.Hkv, group = int(blockIdx.x) / p.Hkv, j = int(blockIdx.x) - group * p.Hkv;
+  const Share share = share_of(total, groups);
+  if (group >= share.groups) return;
+  const int64_t u0 = share.begin(group), u1 = share.begin(group + 1);
+  // the sequence of unit u0: every warp searches for itself, 32 sequences at a time
+  int b = 0;
+  int64_t seg0 = 0;  // its first unit
+  for (;; b += 32) {
+    const int64_t n = b + lane < p.B ? int64_t(units_of(tokens_of(p, b + lane, false))) : 0;
+    int64_t to = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, to, o);
+      if (lane >= o) to += y;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, seg0 + to > u0);
+    if (past != 0u) {
+      const int l = __ffs(past) - 1;
+      seg0 += __shfl_sync(0xffffffffu, to - n, l);
+      b += l;
+      break;
+    }
+    seg0 += __shfl_sync(0xffffffffu, to, 31);
+  }
+  int len = tokens_of(p, b, false), units = units_of(len);
 
   const uint32_t ring = smem_addr(smem) + warp * kStages * C::kStageBytes;
   const uint32_t bars = smem_addr(sBar + warp * kStages);
+  const uint32_t q_s = smem_addr(sQ);
+  const int g8 = lane >> 2, t4 = lane & 3;
+  int stage = 0;
+  uint32_t phase = 0;
+  for (int64_t u = u0; u < u1;) {
+  const int64_t seg1 = seg0 + units, end = min(seg1, u1);
+  const int s0 = int(u - seg0) * kUnit, s1 = int(min(int64_t(len), (end - seg0) * kUnit));
+  const int h0 = j * p.G;
   const uint8_t* kg = p.k + j * p.k_sh;
   const uint8_t* vg = p.v + j * p.v_sh;
-  const int subs = (s1 - s0 + kSub - 1) / kSub;  // sub-tiles of the split; warp w takes w, w + 2, ...
+  const int subs = (s1 - s0 + kSub - 1) / kSub;  // sub-tiles of the piece; warp w takes w, w + 2, ...
   uint32_t valid[kStages];                       // one bit per slot of the stage's sub-tile
 
   // Lanes 0-15 copy the sub-tile's K rows, lanes 16-31 its V rows.  Slots past the end or
@@ -102,7 +184,11 @@ __global__ void __launch_bounds__(kDecodeThreads) qsa_paged_decode_kernel(const 
     bool ok = i < s1;
     int64_t slot = 0;
     if (ok) {
-      const int m = i / p.page_size;
+      int m = i;
+      if (p.page_size > 1) {
+        m = __umulhi(uint32_t(i), p.page_magic);  // i / page_size, or one more
+        if (int64_t(m) * p.page_size > i) --m;
+      }
       const int page = __ldg(p.table + b * p.table_st + m);
       ok = page >= 0 && page < p.pages;
       if (!ok && p.err_word != nullptr) atomicOr(p.err_word, QSA_ERRBIT_SLOT_RANGE);
@@ -116,14 +202,17 @@ __global__ void __launch_bounds__(kDecodeThreads) qsa_paged_decode_kernel(const 
       bulk_copy(ring + stage * C::kStageBytes + lane * C::kPitch,
                lane < 16 ? kg + slot * p.k_ss : vg + slot * p.v_ss, C::kRow, bar);
   };
+  valid[0] = valid[1] = 0;
 #pragma unroll
   for (int s = 0; s < kStages; ++s) {
-    valid[s] = 0;
-    if (warp + s * kDecodeWarps < subs) issue(warp + s * kDecodeWarps, s, valid[s]);
+    if (warp + s * kDecodeWarps < subs) {
+      uint32_t mk;
+      issue(warp + s * kDecodeWarps, stage ^ s, mk);
+      if ((stage ^ s) == 0) valid[0] = mk; else valid[1] = mk;
+    }
   }
 
   // ---- Q: bf16 rows, or f16 for an E4M3 cache (its codes are exact in f16) -----------------
-  const uint32_t q_s = smem_addr(sQ);
   for (int i = tid; i < NT * 8 * (kD / 8); i += kDecodeThreads) {
     const int g = i / (kD / 8), c = i % (kD / 8);
     uint4 raw = make_uint4(0u, 0u, 0u, 0u);
@@ -151,11 +240,8 @@ __global__ void __launch_bounds__(kDecodeThreads) qsa_paged_decode_kernel(const 
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
   }
-  const int g8 = lane >> 2, t4 = lane & 3;
   bool late = false;
 
-  int stage = 0;
-  uint32_t phase = 0;
   for (int sub = warp; sub < subs; sub += kDecodeWarps) {
     const uint32_t kbuf = ring + stage * C::kStageBytes, vbuf = kbuf + kSub * C::kPitch;
     const uint32_t mask = stage == 0 ? valid[0] : valid[1];
@@ -363,50 +449,68 @@ __global__ void __launch_bounds__(kDecodeThreads) qsa_paged_decode_kernel(const 
     // (no slot: every page of the split lies outside the pool)
     const float inv = top == kNegInf ? 0.f : p.v_scale / l;
     const float lse = top == kNegInf ? kNegInf : top + fast_log2(l);
-    const int64_t row = int64_t(b) * p.Hq + h0 + g;
-    if (p.nsplit == 1) {
+    if (seg0 >= u0 && seg1 <= u1) {  // the whole sequence
       *reinterpret_cast<uint2*>(p.out + b * p.o_sb + (h0 + g) * p.o_sh + d) =
           make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-      if (d == 0 && p.lse != nullptr) p.lse[row] = lse;
+      if (d == 0 && p.lse != nullptr) p.lse[int64_t(b) * p.Hq + h0 + g] = lse;
     } else {
-      *reinterpret_cast<float4*>(p.ws_o + (row * p.nsplit + split) * kD + d) =
+      const int64_t rec = (int64_t(blockIdx.x) * 2 + (u == u0 ? 0 : 1)) * p.G + g;
+      *reinterpret_cast<float4*>(p.ws_o + rec * kD + d) =
           make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
-      if (d == 0) p.ws_lse[row * p.nsplit + split] = lse;
+      if (d == 0) p.ws_lse[rec] = lse;
     }
+  }
+  u = end;
+  if (u < u1) {  // the next sequence
+    fence_proxy_async_smem();  // the ring held the merge
+    __syncthreads();
+    seg0 = seg1;
+    do ++b; while (tokens_of(p, b, false) == 0);
+    len = tokens_of(p, b, false);
+    units = units_of(len);
+  }
   }
 }
 
-// Joins the splits of one (sequence, head): 64 dimensions per thread block, 16 lanes of four
-// dimensions by 16 parts of the splits; the parts are added in a fixed order.
-__global__ void __launch_bounds__(kJoinThreads) qsa_paged_join_kernel(const DecodeParams p) {
-  __shared__ float4 sPart[16][16];
-  __shared__ float sRed[kJoinThreads / 32], sSum[16];
+// Joins the pieces of one (sequence, head): 64 lanes of four dimensions by THREADS / 64 parts
+// of the pieces; the parts are added in a fixed order.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) qsa_paged_join_kernel(const DecodeParams p, int groups) {
+  constexpr int kParts = THREADS / 64;
+  __shared__ float4 sPart[kParts][64];
+  __shared__ float sRed[THREADS / 32], sSum[kParts];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int quarter = blockIdx.x & 3;
-  const int64_t row = blockIdx.x >> 2;
-  const int b = int(row / p.Hq), h = int(row % p.Hq);
-  const int len = tokens_of(p, b, false);
-  const int n = int((int64_t(len) + p.split_len - 1) / p.split_len);  // splits that hold tokens
-  const float* lse = p.ws_lse + row * p.nsplit;
+  const int b = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq, j = h / p.G, g = h - j * p.G;
+  const int units = units_of(tokens_of(p, b, false));
+  int64_t total;
+  const int64_t seg0 = units_before(p, b, total, false), seg1 = seg0 + units;
+  const Share share = share_of(total, groups);
+  int first = 0, n = 0;
+  if (units > 0) first = share.owner(seg0), n = share.owner(seg1 - 1) - first + 1;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (n <= 1) return;  // written whole
+  // the first block's piece is its last unless it begins with it; the others begin with theirs
+  const int shift = share.begin(first) < seg0 ? 1 : 0;
+  auto record = [&](int i) { return (((int64_t(first) + i) * p.Hkv + j) * 2 + (i == 0 ? shift : 0)) * p.G + g; };
   float top = kNegInf;
-  for (int s = tid; s < n; s += kJoinThreads) top = fmaxf(top, lse[s]);
+  for (int i = tid; i < n; i += THREADS) top = fmaxf(top, __ldcg(p.ws_lse + record(i)));
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
   if (lane == 0) sRed[warp] = top;
   __syncthreads();
   top = sRed[0];
 #pragma unroll
-  for (int w = 1; w < kJoinThreads / 32; ++w) top = fmaxf(top, sRed[w]);
+  for (int w = 1; w < THREADS / 32; ++w) top = fmaxf(top, sRed[w]);
 
-  const int part = tid >> 4, l = tid & 15;
-  const float* src = p.ws_o + row * p.nsplit * kD + quarter * 64 + l * 4;
+  const int part = tid >> 6, l = tid & 63;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
 #pragma unroll 4
-  for (int s = part; s < n; s += 16) {
-    const float ls = lse[s];
-    const float4 x = *reinterpret_cast<const float4*>(src + int64_t(s) * kD);
-    if (ls == kNegInf) continue;  // a split without a valid page
+  for (int i = part; i < n; i += kParts) {
+    const int64_t rec = record(i);
+    const float ls = __ldcg(p.ws_lse + rec);
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(p.ws_o + rec * kD + l * 4));
+    if (ls == kNegInf) continue;  // a piece without a valid page
     const float f = fast_exp2(ls - top);
     sum += f;
     acc.x = fmaf(x.x, f, acc.x);
@@ -417,11 +521,11 @@ __global__ void __launch_bounds__(kJoinThreads) qsa_paged_join_kernel(const Deco
   sPart[part][l] = acc;
   if (l == 0) sSum[part] = sum;
   __syncthreads();
-  if (tid >= 16) return;
+  if (tid >= 64) return;
   float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
   float l_all = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < kParts; ++i) {
     const float4 x = sPart[i][tid];
     t.x += x.x;
     t.y += x.y;
@@ -430,44 +534,40 @@ __global__ void __launch_bounds__(kJoinThreads) qsa_paged_join_kernel(const Deco
     l_all += sSum[i];
   }
   const float inv = l_all > 0.f || l_all != l_all ? 1.f / l_all : 0.f;
-  *reinterpret_cast<uint2*>(p.out + b * p.o_sb + h * p.o_sh + quarter * 64 + tid * 4) =
+  *reinterpret_cast<uint2*>(p.out + b * p.o_sb + h * p.o_sh + tid * 4) =
       make_uint2(pack_bf16x2(t.x * inv, t.y * inv), pack_bf16x2(t.z * inv, t.w * inv));
-  if (quarter == 0 && tid == 0 && p.lse != nullptr)
-    p.lse[row] = top == kNegInf ? kNegInf : top + fast_log2(l_all);
+  if (tid == 0 && p.lse != nullptr)
+    p.lse[int64_t(b) * p.Hq + h] = top == kNegInf ? kNegInf : top + fast_log2(l_all);
 }
 
 struct DecodePlan {
-  int32_t nsplit, split_len;
+  int32_t blocks;
   size_t lse_offset, bytes;
 };
 
-DecodePlan decode_plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t P, int32_t page_size,
+DecodePlan decode_plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t P, int32_t page_size, int32_t kv_fp8,
                        int32_t num_sms, int32_t request) {
-  const int64_t cap = int64_t(P) * page_size;  // tokens of a sequence at most
-  int64_t n;
-  if (request > 0) {
-    n = request;
-  } else {
-    // four waves of three blocks per SM, so that sequences of different lengths even out
-    const int64_t units = int64_t(B) * Hkv, want = int64_t(num_sms > 0 ? num_sms : 1) * 3;
-    n = units > 0 ? (want * (units * 2 > want ? 4 : 1) + units - 1) / units : 1;
-  }
-  const int64_t most = (cap + kMinSplit - 1) / kMinSplit;
+  const int G = Hq / Hkv;
+  const int resident = kv_fp8 ? (G <= 8 ? Decode<true, 1>::kResident : Decode<true, 2>::kResident)
+                              : (G <= 8 ? Decode<false, 1>::kResident : Decode<false, 2>::kResident);
+  // groups of a block per KV head; no more of them than have kMinUnits units when every
+  // sequence is as long as its pages
+  const int64_t cap = (int64_t(P) * page_size + kUnit - 1) / kUnit;
+  const int64_t most = (int64_t(B) * cap + kMinUnits - 1) / kMinUnits;
+  int64_t n = (request > 0 ? request : int64_t(num_sms > 0 ? num_sms : 1) * resident) / Hkv;
   n = n > most ? most : n;
   n = n < 1 ? 1 : n;
-  int64_t len = cap > 0 ? ((cap + n - 1) / n + kSub - 1) / kSub * kSub : kSub;
-  n = cap > 0 ? (cap + len - 1) / len : 1;
-  DecodePlan pl{int32_t(n), int32_t(len), 0, 0};
+  DecodePlan pl{int32_t(n * Hkv), 0, 0};
   if (n > 1) {
-    const size_t rows = size_t(B) * size_t(Hq) * size_t(n);
-    pl.lse_offset = (rows * kD * 4 + 255) / 256 * 256;
-    pl.bytes = pl.lse_offset + (rows * 4 + 255) / 256 * 256;
+    const size_t records = size_t(pl.blocks) * 2 * size_t(G);
+    pl.lse_offset = records * kD * 4;
+    pl.bytes = pl.lse_offset + (records * 4 + 255) / 256 * 256;
   }
   return pl;
 }
 
 qsa_status_t check_decode_sizes(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t P,
-                                int32_t page_size, int32_t nsplit) {
+                                int32_t page_size, int32_t kv_fp8, int32_t blocks) {
   if (B < 0 || P < 0) QSA_REJECT(QSA_ERR_INVALID_ARG, "negative size: B=%d P=%d", B, P);
   if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0)
     QSA_REJECT(QSA_ERR_INVALID_ARG, "Hq=%d must be a positive multiple of Hkv=%d", Hq, Hkv);
@@ -476,31 +576,47 @@ qsa_status_t check_decode_sizes(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, i
   if (page_size < 1) QSA_REJECT(QSA_ERR_INVALID_ARG, "page_size=%d", page_size);
   if (int64_t(P) * page_size > INT32_MAX - 4096)
     QSA_REJECT(QSA_ERR_UNSUPPORTED, "a page table of %lld tokens", (long long)(int64_t(P) * page_size));
-  if (nsplit < 0) QSA_REJECT(QSA_ERR_INVALID_ARG, "negative nsplit");
+  if (blocks < 0 || blocks > (1 << 16)) QSA_REJECT(QSA_ERR_INVALID_ARG, "blocks=%d outside 0..65536", blocks);
+  if (kv_fp8 != 0 && kv_fp8 != 1) QSA_REJECT(QSA_ERR_INVALID_ARG, "kv_fp8 must be 0 or 1");
   return QSA_OK;
 }
 
 template <bool FP8, int NT>
-cudaError_t launch_decode(const DecodeParams& p, cudaStream_t st) {
+cudaError_t launch_decode(const DecodeParams& p, int blocks, cudaStream_t st) {
   using C = Decode<FP8, NT>;
   const cudaError_t e = cudaFuncSetAttribute(qsa_paged_decode_kernel<FP8, NT>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::kSmem));
   if (e != cudaSuccess) return e;
-  qsa_paged_decode_kernel<FP8, NT><<<unsigned(p.B) * p.Hkv * p.nsplit, kDecodeThreads, C::kSmem, st>>>(p);
+  qsa_paged_decode_kernel<FP8, NT><<<blocks, kDecodeThreads, C::kSmem, st>>>(p);
   return cudaGetLastError();
+}
+
+// Launched while the decode kernel still runs: its blocks wait for that grid's end.
+template <int THREADS>
+cudaError_t launch_join(const DecodeParams& p, int groups, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(p.B) * p.Hq);
+  cfg.blockDim = dim3(THREADS);
+  cfg.stream = st;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, qsa_paged_join_kernel<THREADS>, p, groups);
 }
 
 }  // namespace
 
 extern "C" int32_t qsa_paged_decode_plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t P,
-                                         int32_t page_size, int32_t num_sms,
-                                         int32_t nsplit_request, size_t* workspace_bytes) {
+                                         int32_t page_size, int32_t kv_fp8, int32_t num_sms,
+                                         int32_t blocks_request, size_t* workspace_bytes) {
   set_error_detail("%s", "");
-  const qsa_status_t st = check_decode_sizes(B, Hq, Hkv, D, P, page_size, nsplit_request);
+  const qsa_status_t st = check_decode_sizes(B, Hq, Hkv, D, P, page_size, kv_fp8, blocks_request);
   if (st != QSA_OK) return -int32_t(st);
-  const DecodePlan pl = decode_plan(B, Hq, Hkv, P, page_size, num_sms, nsplit_request);
+  const DecodePlan pl = decode_plan(B, Hq, Hkv, P, page_size, kv_fp8, num_sms, blocks_request);
   if (workspace_bytes != nullptr) *workspace_bytes = pl.bytes;
-  return pl.nsplit;
+  return pl.blocks;
 }
 
 extern "C" qsa_status_t qsa_paged_decode(
@@ -509,11 +625,10 @@ extern "C" qsa_status_t qsa_paged_decode(
     const int32_t* page_table, int64_t page_stride, const int32_t* seq_lens, int32_t B, int32_t Hq,
     int32_t Hkv, int32_t D, int32_t P, int64_t pages, int32_t page_size, float scale, int32_t kv_fp8,
     float k_scale, float v_scale, void* out, int64_t out_stride_b, int64_t out_stride_h, float* lse,
-    int32_t nsplit, void* workspace, size_t workspace_bytes, uint32_t* err_word, void* stream) {
+    int32_t blocks, void* workspace, size_t workspace_bytes, uint32_t* err_word, void* stream) {
   set_error_detail("%s", "");
-  const qsa_status_t sizes = check_decode_sizes(B, Hq, Hkv, D, P, page_size, nsplit);
+  const qsa_status_t sizes = check_decode_sizes(B, Hq, Hkv, D, P, page_size, kv_fp8, blocks);
   if (sizes != QSA_OK) return sizes;
-  if (kv_fp8 != 0 && kv_fp8 != 1) QSA_REJECT(QSA_ERR_INVALID_ARG, "kv_fp8 must be 0 or 1");
   if (!std::isfinite(scale)) QSA_REJECT(QSA_ERR_INVALID_ARG, "scale is not finite");
   if (kv_fp8 && (!std::isfinite(k_scale) || !std::isfinite(v_scale)))
     QSA_REJECT(QSA_ERR_INVALID_ARG, "k_scale or v_scale is not finite");
@@ -533,16 +648,15 @@ extern "C" qsa_status_t qsa_paged_decode(
       !stride_multiple(v_stride_s, e, 16) || !stride_multiple(v_stride_h, e, 16) || page_stride < 0)
     QSA_REJECT(QSA_ERR_INVALID_ARG, "strides must be non-negative multiples of 16 bytes");
   int dev = 0, num_sms = 0;
-  if (nsplit == 0) {
+  if (blocks == 0) {
     cudaError_t ce = cudaGetDevice(&dev);
     if (ce == cudaSuccess) ce = cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev);
     if (ce != cudaSuccess) return launch_status(ce, "qsa_paged_decode");
   }
-  const DecodePlan pl = decode_plan(B, Hq, Hkv, P, page_size, num_sms, nsplit);
-  if (int64_t(B) * Hkv * pl.nsplit > INT32_MAX || int64_t(B) * Hq * 4 > INT32_MAX)
-    QSA_REJECT(QSA_ERR_INVALID_ARG, "too many work units for one launch");
+  const DecodePlan pl = decode_plan(B, Hq, Hkv, P, page_size, kv_fp8, num_sms, blocks);
+  if (int64_t(B) * Hq > INT32_MAX) QSA_REJECT(QSA_ERR_INVALID_ARG, "too many (sequence, head) pairs for one launch");
   if (pl.bytes > 0 && (workspace == nullptr || workspace_bytes < pl.bytes))
-    QSA_REJECT(QSA_ERR_WORKSPACE, "workspace of %zu bytes needed for nsplit=%d, got %zu", pl.bytes, pl.nsplit,
+    QSA_REJECT(QSA_ERR_WORKSPACE, "workspace of %zu bytes needed for blocks=%d, got %zu", pl.bytes, pl.blocks,
                workspace == nullptr ? size_t(0) : workspace_bytes);
   if (!aligned_to(workspace, 16)) QSA_REJECT(QSA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
 
@@ -560,17 +674,17 @@ extern "C" qsa_status_t qsa_paged_decode(
   p.table_st = page_stride, p.pages = pages;
   p.k_ss = k_stride_s * e, p.k_sh = k_stride_h * e, p.v_ss = v_stride_s * e, p.v_sh = v_stride_h * e;
   p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv, p.P = P, p.page_size = page_size;
-  p.nsplit = pl.nsplit, p.split_len = pl.split_len;
+  p.page_magic = uint32_t(((uint64_t(1) << 32) + page_size - 1) / page_size);
   // log2(e): the softmax runs in base 2
   p.scale_log2 = (kv_fp8 ? scale * k_scale : scale) * 1.4426950408889634f;
   p.v_scale = kv_fp8 ? v_scale : 1.0f;
   const auto st = static_cast<cudaStream_t>(stream);
-  cudaError_t ce = kv_fp8 ? (p.G <= 8 ? launch_decode<true, 1>(p, st) : launch_decode<true, 2>(p, st))
-                          : (p.G <= 8 ? launch_decode<false, 1>(p, st) : launch_decode<false, 2>(p, st));
+  const int n = pl.blocks;
+  cudaError_t ce = kv_fp8 ? (p.G <= 8 ? launch_decode<true, 1>(p, n, st) : launch_decode<true, 2>(p, n, st))
+                          : (p.G <= 8 ? launch_decode<false, 1>(p, n, st) : launch_decode<false, 2>(p, n, st));
   if (ce != cudaSuccess) return launch_status(ce, "qsa_paged_decode");
-  if (pl.nsplit > 1) {
-    qsa_paged_join_kernel<<<unsigned(B) * Hq * 4, kJoinThreads, 0, st>>>(p);
-    ce = cudaGetLastError();
-  }
+  // 16 pieces of a sequence or more on average: more parts of them at once
+  const int groups = n / Hkv;
+  if (groups > 1) ce = groups >= 16 * B ? launch_join<1024>(p, groups, st) : launch_join<128>(p, groups, st);
   return launch_status(ce, "qsa_paged_decode: join");
 }

@@ -332,7 +332,7 @@ PyObject* select_slots(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// q, k_cache, v_cache, page_table, seq_lens, page_size, scale, k_scale, v_scale, out, lse, nsplit,
+// q, k_cache, v_cache, page_table, seq_lens, page_size, scale, k_scale, v_scale, out, lse, blocks,
 // workspace, err_word -> out
 PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded("paged_decode", n, 14, [&]() -> PyObject* {
@@ -357,7 +357,7 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
       check("lse", *lse, kF32, device, {B, Hq});
       if (!lse->is_contiguous()) refuse("lse must be contiguous");
     }
-    const int32_t page = whole32("page_size", a[5]), request = whole32("nsplit", a[11]);
+    const int32_t page = whole32("page_size", a[5]), request = whole32("blocks", a[11]);
     if (page < 1) refuse("page_size must be positive");
     const float scale = a[6] == Py_None ? float(1.0 / std::sqrt(double(D))) : real(a[6]);
     const float ks = real(a[7]), vs = real(a[8]);
@@ -365,9 +365,9 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t b = size32("B", B), hq = size32("Hq", Hq), hkv = size32("Hkv", Hkv), d = size32("D", D),
                   p = size32("P", P);
     size_t need = 0;
-    const int32_t nsplit = qsa_paged_decode_plan(
-        b, hq, hkv, d, p, page, at::cuda::getCurrentDeviceProperties()->multiProcessorCount, request, &need);
-    if (nsplit < 0) return PyLong_FromLong(-nsplit);
+    const int32_t blocks = qsa_paged_decode_plan(
+        b, hq, hkv, d, p, page, fp8 ? 1 : 0, at::cuda::getCurrentDeviceProperties()->multiProcessorCount, request, &need);
+    if (blocks < 0) return PyLong_FromLong(-blocks);
     const Tensor *given = maybe("out", a[9]), *given_work = maybe("workspace", a[12]);
     if (given != nullptr) check("out", *given, kBF16, device, {B, Hq, D});
     if (given_work != nullptr) check_dims("workspace", *given_work, kU8, device, 1);
@@ -376,7 +376,7 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const qsa_status_t st = qsa_paged_decode(
         q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
         v.stride(1), ptr32(&table), table.stride(0), ptr32(&lens), b, hq, hkv, d, p, S / page, page, scale, fp8 ? 1 : 0,
-        ks, vs, out.data_ptr(), out.stride(0), out.stride(1), static_cast<float*>(ptr(lse)), nsplit,
+        ks, vs, out.data_ptr(), out.stride(0), out.stride(1), static_cast<float*>(ptr(lse)), blocks,
         work.defined() ? work.data_ptr() : nullptr, work.defined() ? size_t(work.numel()) : 0, err, stream_of(device));
     if (st != QSA_OK) return status(st);
     if (given != nullptr) {

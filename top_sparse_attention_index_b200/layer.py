@@ -102,18 +102,18 @@ def select_slots(q, weight, codes, scales, page_table, seq_lens, top_blocks, pag
                  block, cu_q, sink_blocks, local_blocks, slot_idx, width, workspace, err_word)
 
 
-def qsa_paged_decode_plan(B, Hq, Hkv, D, P, page_size, num_sms, nsplit_request=0):
-    """(nsplit, workspace_bytes) for this shape; raises QSAError for invalid shapes."""
+def qsa_paged_decode_plan(B, Hq, Hkv, D, P, page_size, kv_fp8, num_sms, blocks_request=0):
+    """(blocks, workspace_bytes) for this shape; raises QSAError for invalid shapes."""
     ws = ctypes.c_size_t(0)
-    n = int(load_library().qsa_paged_decode_plan(B, Hq, Hkv, D, P, page_size, num_sms,
-                                                 nsplit_request, ctypes.byref(ws)))
+    n = int(load_library().qsa_paged_decode_plan(B, Hq, Hkv, D, P, page_size, 1 if kv_fp8 else 0,
+                                                 num_sms, blocks_request, ctypes.byref(ws)))
     if n < 0:
         raise QSAError(-n, qsa_last_error_detail())
     return n, int(ws.value)
 
 
 def paged_decode(q, k_cache, v_cache, page_table, seq_lens, page_size, scale=None, k_scale=1.0,
-                 v_scale=1.0, out=None, lse=None, nsplit=0, workspace=None, err_word=None,
+                 v_scale=1.0, out=None, lse=None, blocks=0, workspace=None, err_word=None,
                  stream=None):
     """Attention of one new token per sequence over its whole paged cache.
 
@@ -124,4 +124,4 @@ def paged_decode(q, k_cache, v_cache, page_table, seq_lens, page_size, scale=Non
     (float32 [B, Hq], optional) receives the base-2 log-sum-exp of the scaled scores.
     """
     return _call("paged_decode", stream, q, k_cache, v_cache, page_table, seq_lens, page_size, scale, k_scale,
-                 v_scale, out, lse, nsplit, workspace, err_word)
+                 v_scale, out, lse, blocks, workspace, err_word)
