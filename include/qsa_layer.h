@@ -32,8 +32,8 @@ extern "C" {
 #define QSA_MAX_INDEX_HEADS 64
 #define QSA_MAX_TOP_BLOCKS 8192
 
-/* A further bit of *err_word: a bounded wait of qsa_select_slots or qsa_paged_decode for its
- * own copies or products ran out (the device was stopped or is failing); the output is not
+/* A further bit of *err_word: a bounded wait of qsa_select_slots for its own copies or
+ * products ran out (the device was stopped or is failing); the output is not
  * valid. */
 #define QSA_ERRBIT_TIMEOUT 0x10u
 
@@ -158,8 +158,8 @@ qsa_status_t qsa_select_slots(const void* q, int64_t q_stride_t, int64_t q_strid
  * evenly over the thread blocks; pieces of one sequence are joined by their log-sum-exp.
  *
  *   q            bf16 [B, Hq, D], strides (b, h);  out bf16 [B, Hq, D].
- *   k_cache, v_cache   [pages * page_size, Hkv, D]: bf16, or E4M3 codes with kv_fp8
- *                (strides in bytes), dequantised as code * k_scale (v_scale).
+ *   k_cache, v_cache   [pages * page_size, Hkv, D] (fewer than 2^31 slots, their strides
+ *                below 2^30 elements): bf16, or E4M3 codes with kv_fp8 (strides in bytes), dequantised as code * k_scale (v_scale).
  *   page_table   int32 [B, P], row stride page_stride.  A page outside [0, pages) sets
  *                QSA_ERRBIT_SLOT_RANGE; its tokens are masked.
  *   seq_lens     int32 [B]; values outside [0, P page_size] are clamped and set

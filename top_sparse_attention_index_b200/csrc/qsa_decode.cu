@@ -24,7 +24,8 @@ struct DecodeParams {
   float *lse, *ws_o, *ws_lse;  // ws_o [blocks, 2, G, D], ws_lse [blocks, 2, G]
   uint32_t* err_word;
   int64_t q_sb, q_sh, o_sb, o_sh, table_st, pages;
-  int64_t k_ss, k_sh, v_ss, v_sh;  // bytes
+  uint32_t k_ss, v_ss;  // bytes
+  int64_t k_sh, v_sh;   // bytes
   int32_t B, Hq, Hkv, G, P, page_size;
   uint32_t page_magic;  // 2^32 / page_size, rounded up
   float scale_log2, v_scale;
@@ -106,8 +107,8 @@ struct Decode {
 // output, a piece of one to the block's record (its first piece to record 0, its last to
 // record 1: pieces between them are whole sequences).
 // Within a block each warp takes every second 16-slot sub-tile and runs a pipeline of its
-// own: one bulk copy per K or V row and lane, an mbarrier per stage, no block-wide barrier in
-// the loop.  Scores are S^T = K Q^T with the slots as M and the heads as N, so the group
+// own: asynchronous copies into a stage while it works on the other, no block-wide barrier
+// in the loop.  Scores are S^T = K Q^T with the slots as M and the heads as N, so the group
 // shares every row that is read; the softmax is online (base 2, the reference moves only when
 // the maximum rises by more than 2^8); P is rounded to 16 bits for O^T += V^T P^T, and the
 // denominator sums the same rounded values.  The bound is HBM: every row is read once.
@@ -115,18 +116,12 @@ template <bool FP8, int NT>
 __global__ void __launch_bounds__(kDecodeThreads) qsa_paged_decode_kernel(const DecodeParams p) {
   using C = Decode<FP8, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t sBar[kDecodeWarps * kStages];
   __shared__ float2 sState[kDecodeWarps][NT * 8];  // (m, l) of each warp and head
   uint8_t* sQ = smem + C::kRing;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the join waits for this grid's end)
-  if (tid == 0) {
-    for (int i = 0; i < kDecodeWarps * kStages; ++i) mbar_init(smem_addr(sBar + i), 1);
-    mbar_init_fence();
-  }
   int64_t total;
   units_before(p, 0, total, blockIdx.x == 0 && warp == 0);
-  __syncthreads();  // the mbarriers
   // sequences without a token: zeros
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
     if (tokens_of(p, b, false) > 0) continue;
@@ -163,11 +158,9 @@ __global__ void __launch_bounds__(kDecodeThreads) qsa_paged_decode_kernel(const 
   int len = tokens_of(p, b, false), units = units_of(len);
 
   const uint32_t ring = smem_addr(smem) + warp * kStages * C::kStageBytes;
-  const uint32_t bars = smem_addr(sBar + warp * kStages);
   const uint32_t q_s = smem_addr(sQ);
   const int g8 = lane >> 2, t4 = lane & 3;
   int stage = 0;
-  uint32_t phase = 0;
   for (int64_t u = u0; u < u1;) {
   const int64_t seg1 = seg0 + units, end = min(seg1, u1);
   const int s0 = int(u - seg0) * kUnit, s1 = int(min(int64_t(len), (end - seg0) * kUnit));
@@ -177,12 +170,18 @@ __global__ void __launch_bounds__(kDecodeThreads) qsa_paged_decode_kernel(const 
   const int subs = (s1 - s0 + kSub - 1) / kSub;  // sub-tiles of the piece; warp w takes w, w + 2, ...
   uint32_t valid[kStages];                       // one bit per slot of the stage's sub-tile
 
-  // Lanes 0-15 copy the sub-tile's K rows, lanes 16-31 its V rows.  Slots past the end or
-  // in a page outside the pool are not read.
-  auto issue = [&](int sub, int stage, uint32_t& mask) {
+  // The sub-tile's rows, 16 bytes per lane and copy: a row is kRow / 16 lanes.  Lane r looks up
+  // slot r; rows past the end or in a page outside the pool are not read, and become zeros.
+  // (One bulk copy per row, issued by its own lane, cost more instructions than everything
+  // else here: 235 us for 1.07 GB of E4M3 rows.)
+  constexpr int kRowLanes = C::kRow / 16, kRows = 32 / kRowLanes;  // lanes of a row, rows of a copy
+  const uint8_t* kl = kg + (lane % kRowLanes) * 16;
+  const uint8_t* vl = vg + (lane % kRowLanes) * 16;
+  const uint32_t to_lane = ring + (lane / kRowLanes) * C::kPitch + (lane % kRowLanes) * 16;
+  auto issue = [&](int sub, int to) -> uint32_t {
     const int i = s0 + sub * kSub + (lane & 15);
     bool ok = i < s1;
-    int64_t slot = 0;
+    int slot = 0;
     if (ok) {
       int m = i;
       if (p.page_size > 1) {
@@ -192,24 +191,28 @@ __global__ void __launch_bounds__(kDecodeThreads) qsa_paged_decode_kernel(const 
       const int page = __ldg(p.table + b * p.table_st + m);
       ok = page >= 0 && page < p.pages;
       if (!ok && p.err_word != nullptr) atomicOr(p.err_word, QSA_ERRBIT_SLOT_RANGE);
-      slot = int64_t(page) * p.page_size + (i - m * p.page_size);
+      slot = ok ? page * p.page_size + (i - m * p.page_size) : 0;
     }
-    mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
-    const uint32_t bar = bars + stage * 8;
-    if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(__popc(mask)) * 2 * C::kRow);
-    __syncwarp();
-    if (ok)
-      bulk_copy(ring + stage * C::kStageBytes + lane * C::kPitch,
-               lane < 16 ? kg + slot * p.k_ss : vg + slot * p.v_ss, C::kRow, bar);
+    const uint32_t mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+    const uint32_t dst = to_lane + to * C::kStageBytes;
+#pragma unroll
+    for (int r = 0; r < kSub; r += kRows) {
+      const int row = r + lane / kRowLanes;
+      const uint32_t from = uint32_t(__shfl_sync(0xffffffffu, slot, row));
+      const bool there = (mask >> row) & 1;
+      cp_async_16(dst + r * C::kPitch, kl + uint64_t(from) * p.k_ss, there);
+      cp_async_16(dst + (kSub + r) * C::kPitch, vl + uint64_t(from) * p.v_ss, there);
+    }
+    return mask;
   };
   valid[0] = valid[1] = 0;
 #pragma unroll
   for (int s = 0; s < kStages; ++s) {
     if (warp + s * kDecodeWarps < subs) {
-      uint32_t mk;
-      issue(warp + s * kDecodeWarps, stage ^ s, mk);
+      const uint32_t mk = issue(warp + s * kDecodeWarps, stage ^ s);
       if ((stage ^ s) == 0) valid[0] = mk; else valid[1] = mk;
     }
+    cp_async_commit();
   }
 
   // ---- Q: bf16 rows, or f16 for an E4M3 cache (its codes are exact in f16) -----------------
@@ -224,38 +227,33 @@ __global__ void __launch_bounds__(kDecodeThreads) qsa_paged_decode_kernel(const 
 #pragma unroll
       for (int e = 0; e < 8; ++e) big |= fabsf(x[e]) >= 65536.f;
       if (big && p.err_word != nullptr) atomicOr(p.err_word, QSA_ERRBIT_Q_RANGE);
-      raw = make_uint4(pack_f16x2(x[0], x[1]), pack_f16x2(x[2], x[3]), pack_f16x2(x[4], x[5]),
-                       pack_f16x2(x[6], x[7]));
+      // K's fragments have codes 4 t .. 4 t + 3 of 16 where the MMA has k = 2 t, 2 t + 1, 2 t + 8,
+      // 2 t + 9: the same order for Q (c is half of 16 dimensions)
+      uint8_t* dst = sQ + g * C::kQPitch + (c >> 1) * 32 + (c & 1) * 8;
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_f16x2(x[0], x[1]), pack_f16x2(x[4], x[5]));
+      *reinterpret_cast<uint2*>(dst + 16) = make_uint2(pack_f16x2(x[2], x[3]), pack_f16x2(x[6], x[7]));
+    } else {
+      *reinterpret_cast<uint4*>(sQ + g * C::kQPitch + c * 16) = raw;
     }
-    *reinterpret_cast<uint4*>(sQ + g * C::kQPitch + c * 16) = raw;
   }
   __syncthreads();
 
   float o[NT][16][4];  // O^T: 16 m-tiles of 16 dimensions
-  float m_ref[NT][2], l_sum[NT][2];
+  float l[NT][4];      // P's sums over the slots: an m-tile whose A is all ones
+  float m_ref[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     m_ref[n][0] = m_ref[n][1] = kNegInf;
-    l_sum[n][0] = l_sum[n][1] = 0.f;
+    l[n][0] = l[n][1] = l[n][2] = l[n][3] = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
   }
-  bool late = false;
 
   for (int sub = warp; sub < subs; sub += kDecodeWarps) {
     const uint32_t kbuf = ring + stage * C::kStageBytes, vbuf = kbuf + kSub * C::kPitch;
     const uint32_t mask = stage == 0 ? valid[0] : valid[1];
-    if (__any_sync(0xffffffffu, !wait_phase(bars + stage * 8, phase))) {
-      late = true;
-      break;
-    }
-    if (mask != 0xffffu) {  // V rows that were not read: zeros, so that 0 * V is 0
-      if (lane >= 16 && !((mask >> (lane - 16)) & 1)) {
-        uint8_t* row = smem + (kbuf - smem_addr(smem)) + lane * C::kPitch;
-        for (int c = 0; c < C::kRow / 16; ++c) reinterpret_cast<uint4*>(row)[c] = make_uint4(0u, 0u, 0u, 0u);
-      }
-      __syncwarp();
-    }
+    cp_async_wait<kStages - 1>();
+    __syncwarp();
 
     // ---- S^T = K Q^T: two accumulators per n8 tile keep two chains in flight ---------------
     float s[NT][2][4];
@@ -263,91 +261,96 @@ __global__ void __launch_bounds__(kDecodeThreads) qsa_paged_decode_kernel(const 
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int c = 0; c < 2; ++c) s[n][c][0] = s[n][c][1] = s[n][c][2] = s[n][c][3] = 0.f;
-    if constexpr (!FP8) {
+    const uint32_t krow = kbuf + (lane & 15) * C::kPitch + (lane >> 4) * 16;
 #pragma unroll
-      for (int ks = 0; ks < 16; ++ks) {
-        uint32_t a[4];
-        ldmatrix_x4(a, kbuf + (lane & 15) * C::kPitch + ks * 32 + (lane >> 4) * 16);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const uint32_t qa = q_s + (n * 8 + g8) * C::kQPitch + ks * 32 + t4 * 4;
-          uint32_t b0, b1;
-          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(b0) : "r"(qa));
-          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(b1) : "r"(qa + 16));
-          mma_bf16_16816(s[n][ks & 1], a, b0, b1);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int kp = 0; kp < 8; ++kp) {  // two 16-code k-steps per load
+    for (int kp = 0; kp < 8; ++kp) {  // two 16-wide k-steps
+      uint32_t b[NT][2][2], a[2][4];  // Q [tile][step], K [step]
+      if constexpr (NT == 1) {
         uint32_t r[4];
-        ldmatrix_x4(r, kbuf + (lane & 15) * C::kPitch + kp * 32 + (lane >> 4) * 16);
+        ldmatrix_x4(r, q_s + (lane & 7) * C::kQPitch + kp * 64 + (lane >> 3) * 16);
+        b[0][0][0] = r[0], b[0][0][1] = r[1], b[0][1][0] = r[2], b[0][1][1] = r[3];
+      } else {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          // the lane's codes 4 t4 .. 4 t4 + 3 of a row stand for k = 2 t4, 2 t4 + 1, 2 t4 + 8,
-          // 2 t4 + 9: a permutation of the sum's order that Q's fragments share
-          uint32_t a[4];
-          e4m3x4_to_f16x2x2(r[2 * e], a[0], a[2]);
-          e4m3x4_to_f16x2x2(r[2 * e + 1], a[1], a[3]);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const uint32_t qa = q_s + (n * 8 + g8) * C::kQPitch + (kp * 2 + e) * 32 + t4 * 8;
-            uint32_t b0, b1;
-            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(b0), "=r"(b1) : "r"(qa));
-            mma_f16_16816(s[n][e], a, b0, b1);
-          }
+          uint32_t r[4];
+          ldmatrix_x4(r, q_s + ((lane >> 4) * 8 + (lane & 7)) * C::kQPitch + (kp * 2 + e) * 32 + ((lane >> 3) & 1) * 16);
+          b[0][e][0] = r[0], b[0][e][1] = r[1], b[NT - 1][e][0] = r[2], b[NT - 1][e][1] = r[3];
         }
       }
+      if constexpr (!FP8) {
+        ldmatrix_x4(a[0], krow + kp * 64);
+        ldmatrix_x4(a[1], krow + kp * 64 + 32);
+      } else {
+        uint32_t r[4];
+        ldmatrix_x4(r, krow + kp * 32);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          e4m3x4_to_f16x2x2(r[2 * e], a[e][0], a[e][2]);
+          e4m3x4_to_f16x2x2(r[2 * e + 1], a[e][1], a[e][3]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if constexpr (FP8) mma_f16_16816(s[n][e], a[e], b[n][e][0], b[n][e][1]);
+          else mma_bf16_16816(s[n][e], a[e], b[n][e][0], b[n][e][1]);
+        }
     }
 
     // ---- softmax over the sub-tile's slots (rows g8 and g8 + 8) ------------------------------
-    const bool ok0 = (mask >> g8) & 1, ok1 = (mask >> (g8 + 8)) & 1;
-    uint32_t pb[NT][2];
+    float x[NT][4], top[NT][2];
+    bool rises = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float x[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float y = (s[n][0][e] + s[n][1][e]) * p.scale_log2;
-        x[e] = (e < 2 ? ok0 : ok1) ? y : kNegInf;
+      for (int e = 0; e < 4; ++e) x[n][e] = (s[n][0][e] + s[n][1][e]) * p.scale_log2;
+      if (mask != 0xffffu) {
+        if (!((mask >> g8) & 1)) x[n][0] = x[n][1] = kNegInf;
+        if (!((mask >> (g8 + 8)) & 1)) x[n][2] = x[n][3] = kNegInf;
       }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float top = fmaxf(x[c], x[c + 2]);
+        top[n][c] = fmaxf(x[n][c], x[n][c + 2]);
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        if (top > m_ref[n][c] + kRescaleLog2 || m_ref[n][c] == kNegInf) {
-          const float f = m_ref[n][c] == kNegInf ? 0.f : fast_exp2(m_ref[n][c] - top);
+        for (int d = 4; d < 32; d <<= 1) top[n][c] = fmaxf(top[n][c], __shfl_xor_sync(0xffffffffu, top[n][c], d));
+        rises |= top[n][c] > m_ref[n][c] + kRescaleLog2 || m_ref[n][c] == kNegInf;
+      }
+    }
+    if (__any_sync(0xffffffffu, rises)) {  // some head's reference moves
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (!(top[n][c] > m_ref[n][c] + kRescaleLog2 || m_ref[n][c] == kNegInf)) continue;
           if (m_ref[n][c] != kNegInf) {
-            l_sum[n][c] *= f;
+            const float f = fast_exp2(m_ref[n][c] - top[n][c]);
+            l[n][c] *= f;
+            l[n][c + 2] *= f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               o[n][i][c] *= f;
               o[n][i][c + 2] *= f;
             }
           }
-          m_ref[n][c] = top;
+          m_ref[n][c] = top[n][c];
         }
       }
+    }
+    uint32_t pb[NT][2];
+    const uint32_t one = FP8 ? 0x3C003C00u : 0x3F803F80u;
+    const uint32_t ones[4] = {one, one, one, one};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float ref = m_ref[n][e & 1];
-        x[e] = ref == kNegInf ? 0.f : fast_exp2(x[e] - ref);
-      }
-      uint32_t lo, hi;  // slots g8 and g8 + 8, heads 2 t4 and 2 t4 + 1
-      if constexpr (FP8) {
-        lo = pack_f16x2(x[0], x[1]);
-        hi = pack_f16x2(x[2], x[3]);
-        l_sum[n][0] += f16lo_to_f32(lo) + f16lo_to_f32(hi);
-        l_sum[n][1] += f16hi_to_f32(lo) + f16hi_to_f32(hi);
-      } else {
-        lo = pack_bf16x2(x[0], x[1]);
-        hi = pack_bf16x2(x[2], x[3]);
-        l_sum[n][0] += bf16lo_to_f32(lo) + bf16lo_to_f32(hi);
-        l_sum[n][1] += bf16hi_to_f32(lo) + bf16hi_to_f32(hi);
-      }
-      pb[n][0] = movmatrix_trans(lo);
-      pb[n][1] = movmatrix_trans(hi);
+    for (int n = 0; n < NT; ++n) {
+      // (a reference of -infinity, where no slot was valid yet: the weights are 0)
+      const float r0 = fmaxf(m_ref[n][0], -3.402823466e38f), r1 = fmaxf(m_ref[n][1], -3.402823466e38f);
+      const float w0 = fast_exp2(x[n][0] - r0), w1 = fast_exp2(x[n][1] - r1);
+      const float w2 = fast_exp2(x[n][2] - r0), w3 = fast_exp2(x[n][3] - r1);
+      // slots g8 and g8 + 8, heads 2 t4 and 2 t4 + 1
+      pb[n][0] = movmatrix_trans(FP8 ? pack_f16x2(w0, w1) : pack_bf16x2(w0, w1));
+      pb[n][1] = movmatrix_trans(FP8 ? pack_f16x2(w2, w3) : pack_bf16x2(w2, w3));
+      if constexpr (FP8) mma_f16_16816(l[n], ones, pb[n][0], pb[n][1]);
+      else mma_bf16_16816(l[n], ones, pb[n][0], pb[n][1]);
     }
 
     // ---- O^T += V^T P^T --------------------------------------------------------------------
@@ -379,42 +382,25 @@ __global__ void __launch_bounds__(kDecodeThreads) qsa_paged_decode_kernel(const 
       }
     }
 
-    // the stage's rows have been read: the next sub-tile may land in it
-    fence_proxy_async_smem();
-    __syncwarp();
+    __syncwarp();  // the stage's rows have been read: the next sub-tile may land in it
     const int next = sub + kStages * kDecodeWarps;
     if (next < subs) {
-      uint32_t mk;
-      issue(next, stage, mk);
+      const uint32_t mk = issue(next, stage);
       if (stage == 0) valid[0] = mk; else valid[1] = mk;
     }
-    if (++stage == kStages) {
-      stage = 0;
-      phase ^= 1;
-    }
+    cp_async_commit();
+    stage ^= 1;
   }
-  if (late) {  // give the copies in flight a second chance to land, then leave without a result
-    if (lane == 0 && p.err_word != nullptr) atomicOr(p.err_word, QSA_ERRBIT_TIMEOUT);
-    wait_phase(bars + stage * 8, phase);
-    wait_phase(bars + (stage ^ 1) * 8, phase ^ uint32_t(stage));
-  }
-  if (__syncthreads_or(late)) return;
 
-  // ---- merge the warps, then the split's record or the output ------------------------------
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int d = 4; d < 32; d <<= 1) l_sum[n][c] += __shfl_xor_sync(0xffffffffu, l_sum[n][c], d);
-  // (both warps are done with the ring and Q: the barrier above)
+  // ---- merge the warps, then the piece's record or the output ------------------------------
+  __syncthreads();  // both warps are done with the ring and the Q rows
   float* sO = reinterpret_cast<float*>(smem);
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int g = n * 8 + 2 * t4 + c;
-      if (g8 == 0) sState[warp][g] = make_float2(m_ref[n][c], l_sum[n][c]);
+      if (g8 == 0) sState[warp][g] = make_float2(m_ref[n][c], l[n][c]);
       float* dst = sO + (warp * NT * 8 + g) * C::kMergePitch;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -433,22 +419,22 @@ __global__ void __launch_bounds__(kDecodeThreads) qsa_paged_decode_kernel(const 
     float top = kNegInf;
 #pragma unroll
     for (int w = 0; w < kDecodeWarps; ++w) top = fmaxf(top, sState[w][g].x);
-    float acc[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
 #pragma unroll
     for (int w = 0; w < kDecodeWarps; ++w) {
       const float2 st = sState[w][g];
       if (st.x == kNegInf) continue;  // this warp saw no slot
       const float f = fast_exp2(st.x - top);
       const float4 x = *reinterpret_cast<const float4*>(sO + (w * NT * 8 + g) * C::kMergePitch + d);
-      l = fmaf(st.y, f, l);
+      sum = fmaf(st.y, f, sum);
       acc[0] = fmaf(x.x, f, acc[0]);
       acc[1] = fmaf(x.y, f, acc[1]);
       acc[2] = fmaf(x.z, f, acc[2]);
       acc[3] = fmaf(x.w, f, acc[3]);
     }
     // (no slot: every page of the split lies outside the pool)
-    const float inv = top == kNegInf ? 0.f : p.v_scale / l;
-    const float lse = top == kNegInf ? kNegInf : top + fast_log2(l);
+    const float inv = top == kNegInf ? 0.f : p.v_scale / sum;
+    const float lse = top == kNegInf ? kNegInf : top + fast_log2(sum);
     if (seg0 >= u0 && seg1 <= u1) {  // the whole sequence
       *reinterpret_cast<uint2*>(p.out + b * p.o_sb + (h0 + g) * p.o_sh + d) =
           make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
@@ -462,8 +448,7 @@ __global__ void __launch_bounds__(kDecodeThreads) qsa_paged_decode_kernel(const 
   }
   u = end;
   if (u < u1) {  // the next sequence
-    fence_proxy_async_smem();  // the ring held the merge
-    __syncthreads();
+    __syncthreads();  // (the ring held the merge)
     seg0 = seg1;
     do ++b; while (tokens_of(p, b, false) == 0);
     len = tokens_of(p, b, false);
@@ -632,7 +617,10 @@ extern "C" qsa_status_t qsa_paged_decode(
   if (!std::isfinite(scale)) QSA_REJECT(QSA_ERR_INVALID_ARG, "scale is not finite");
   if (kv_fp8 && (!std::isfinite(k_scale) || !std::isfinite(v_scale)))
     QSA_REJECT(QSA_ERR_INVALID_ARG, "k_scale or v_scale is not finite");
-  if (pages < 0) QSA_REJECT(QSA_ERR_INVALID_ARG, "negative pages");
+  if (pages < 0 || pages * page_size > INT32_MAX)
+    QSA_REJECT(QSA_ERR_INVALID_ARG, "%lld pages of %d slots: slots are int32", (long long)pages, page_size);
+  if (k_stride_s > INT32_MAX / 2 || v_stride_s > INT32_MAX / 2)
+    QSA_REJECT(QSA_ERR_UNSUPPORTED, "slot strides of 2^30 elements or more");
   if (B == 0) return QSA_OK;
   if (q == nullptr || seq_lens == nullptr || out == nullptr ||
       (P > 0 && (page_table == nullptr || (pages > 0 && (k_cache == nullptr || v_cache == nullptr)))))
@@ -672,7 +660,8 @@ extern "C" qsa_status_t qsa_paged_decode(
   p.err_word = err_word;
   p.q_sb = q_stride_b, p.q_sh = q_stride_h, p.o_sb = out_stride_b, p.o_sh = out_stride_h;
   p.table_st = page_stride, p.pages = pages;
-  p.k_ss = k_stride_s * e, p.k_sh = k_stride_h * e, p.v_ss = v_stride_s * e, p.v_sh = v_stride_h * e;
+  p.k_ss = uint32_t(k_stride_s * e), p.k_sh = k_stride_h * e;
+  p.v_ss = uint32_t(v_stride_s * e), p.v_sh = v_stride_h * e;
   p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv, p.P = P, p.page_size = page_size;
   p.page_magic = uint32_t(((uint64_t(1) << 32) + page_size - 1) / page_size);
   // log2(e): the softmax runs in base 2
