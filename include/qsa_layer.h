@@ -59,8 +59,8 @@ extern "C" {
  *   q_out         bf16 [T, Hq, D].  May be q itself (same pointer and strides).
  *   k_dst, v_dst  [rows, Hkv, D], strides (row, h): token t goes to row slots[t], or to
  *                 row t when slots is NULL (then rows must be >= T; k_dst may be k).
- *                 bf16, or with kv_fp8 E4M3 codes of x / k_scale (x / v_scale), saturated
- *                 (strides in bytes).  slots[t] = -1 stores nothing; another value outside
+ *                 bf16, or with kv_fp8 E4M3 codes of x * (1 / k_scale) (x * (1 / v_scale)),
+ *                 saturated (strides in bytes).  slots[t] = -1 stores nothing; another value outside
  *                 [0, rows) stores nothing and sets QSA_ERRBIT_SLOT_RANGE.  When two tokens
  *                 name one slot, which of them it holds is unspecified.
  *   D is 64, 128 or 256; rot is a multiple of 16, at most D (0: no rotation).

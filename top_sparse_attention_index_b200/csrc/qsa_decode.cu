@@ -7,12 +7,9 @@ namespace {
 using namespace qsa;
 
 constexpr int kD = kHeadDim;
-constexpr int kDecodeWarps = 2;
-constexpr int kDecodeThreads = 32 * kDecodeWarps;
 constexpr int kStages = 2;
 constexpr int kSub = 16;                 // slots of a warp's sub-tile (the M of one MMA)
-constexpr int kUnit = kSub * kDecodeWarps;  // slots that the work is shared out in
-constexpr int kMinUnits = 2;                // of a thread block: what it has in flight at once
+constexpr int kUnit = 64;                // slots that the work is shared out in
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kRescaleLog2 = 8.0f;
 
@@ -57,8 +54,7 @@ struct Share {
 };
 
 __device__ __forceinline__ Share share_of(int64_t total, int groups) {
-  const int64_t most = (total + kMinUnits - 1) / kMinUnits;
-  Share s{0, 0, int32_t(most < groups ? most : groups)};
+  Share s{0, 0, int32_t(total < groups ? total : groups)};
   if (s.groups > 0) {
     s.each = Share::quotient(total, s.groups);
     s.longer = total - s.each * s.groups;
@@ -87,15 +83,20 @@ __device__ __forceinline__ int64_t units_before(const DecodeParams& p, int b, in
 // so the eight rows that one 8x8 matrix load touches fall into different banks.
 template <bool FP8, int NT>
 struct Decode {
+  // Of E4M3 rows twice as many are in flight, and twice the warps work on them (4 x 262,144
+  // tokens: 203 us with two warps to a block, 192 with four; with bf16 rows four warps leave
+  // an SM one block instead of three: 64 ragged sequences 130 us, 118 with two).
+  static constexpr int kWarps = FP8 ? 4 : 2;
+  static constexpr int kThreads = 32 * kWarps;
   static constexpr int kRow = FP8 ? kD : 2 * kD;  // bytes of a cache row
   static constexpr int kPitch = kRow + 16;
   static constexpr int kStageBytes = 2 * kSub * kPitch;  // K rows, then V rows
-  static constexpr int kRing = kDecodeWarps * kStages * kStageBytes;
+  static constexpr int kRing = kWarps * kStages * kStageBytes;
   static constexpr int kQPitch = 2 * kD + 16;
   static constexpr int kQBytes = NT * 8 * kQPitch;
   static constexpr int kMergePitch = kD + 4;
   static constexpr size_t kSmem = kRing + kQBytes;
-  static constexpr int kMergeBytes = kDecodeWarps * NT * 8 * kMergePitch * 4;
+  static constexpr int kMergeBytes = kWarps * NT * 8 * kMergePitch * 4;
   // thread blocks of an SM: 228 KB of shared memory, 1 KB of each block reserved
   static constexpr int kResident = (228 * 1024) / (int(kSmem) + 1024 + 512);
   static_assert(kMergeBytes <= int(kSmem), "the merge buffer reuses the ring and the Q rows");
@@ -106,17 +107,18 @@ struct Decode {
 // sequences took 157 us, so 113); a sequence that one block holds whole is written to the
 // output, a piece of one to the block's record (its first piece to record 0, its last to
 // record 1: pieces between them are whole sequences).
-// Within a block each warp takes every second 16-slot sub-tile and runs a pipeline of its
+// Within a block each warp takes its 16-slot sub-tiles of a unit and runs a pipeline of its
 // own: asynchronous copies into a stage while it works on the other, no block-wide barrier
 // in the loop.  Scores are S^T = K Q^T with the slots as M and the heads as N, so the group
 // shares every row that is read; the softmax is online (base 2, the reference moves only when
 // the maximum rises by more than 2^8); P is rounded to 16 bits for O^T += V^T P^T, and the
 // denominator sums the same rounded values.  The bound is HBM: every row is read once.
 template <bool FP8, int NT>
-__global__ void __launch_bounds__(kDecodeThreads) qsa_paged_decode_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(Decode<FP8, NT>::kThreads) qsa_paged_decode_kernel(const DecodeParams p) {
   using C = Decode<FP8, NT>;
+  constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float2 sState[kDecodeWarps][NT * 8];  // (m, l) of each warp and head
+  __shared__ float2 sState[kWarps][NT * 8];  // (m, l) of each warp and head
   uint8_t* sQ = smem + C::kRing;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the join waits for this grid's end)
@@ -125,11 +127,11 @@ __global__ void __launch_bounds__(kDecodeThreads) qsa_paged_decode_kernel(const 
   // sequences without a token: zeros
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
     if (tokens_of(p, b, false) > 0) continue;
-    for (int i = tid; i < p.Hq * (kD / 8); i += kDecodeThreads)
+    for (int i = tid; i < p.Hq * (kD / 8); i += kThreads)
       *reinterpret_cast<uint4*>(p.out + b * p.o_sb + (i / (kD / 8)) * p.o_sh + (i % (kD / 8)) * 8) =
           make_uint4(0u, 0u, 0u, 0u);
     if (p.lse != nullptr)
-      for (int h = tid; h < p.Hq; h += kDecodeThreads) p.lse[int64_t(b) * p.Hq + h] = kNegInf;
+      for (int h = tid; h < p.Hq; h += kThreads) p.lse[int64_t(b) * p.Hq + h] = kNegInf;
   }
   const int groups = int(gridDim.x) / p.Hkv, group = int(blockIdx.x) / p.Hkv, j = int(blockIdx.x) - group * p.Hkv;
   const Share share = share_of(total, groups);
@@ -167,7 +169,7 @@ __global__ void __launch_bounds__(kDecodeThreads) qsa_paged_decode_kernel(const 
   const int h0 = j * p.G;
   const uint8_t* kg = p.k + j * p.k_sh;
   const uint8_t* vg = p.v + j * p.v_sh;
-  const int subs = (s1 - s0 + kSub - 1) / kSub;  // sub-tiles of the piece; warp w takes w, w + 2, ...
+  const int subs = (s1 - s0 + kSub - 1) / kSub;  // sub-tiles of the piece; warp w takes w, w + kWarps, ...
   uint32_t valid[kStages];                       // one bit per slot of the stage's sub-tile
 
   // The sub-tile's rows, 16 bytes per lane and copy: a row is kRow / 16 lanes.  Lane r looks up
@@ -208,15 +210,15 @@ __global__ void __launch_bounds__(kDecodeThreads) qsa_paged_decode_kernel(const 
   valid[0] = valid[1] = 0;
 #pragma unroll
   for (int s = 0; s < kStages; ++s) {
-    if (warp + s * kDecodeWarps < subs) {
-      const uint32_t mk = issue(warp + s * kDecodeWarps, stage ^ s);
+    if (warp + s * kWarps < subs) {
+      const uint32_t mk = issue(warp + s * kWarps, stage ^ s);
       if ((stage ^ s) == 0) valid[0] = mk; else valid[1] = mk;
     }
     cp_async_commit();
   }
 
   // ---- Q: bf16 rows, or f16 for an E4M3 cache (its codes are exact in f16) -----------------
-  for (int i = tid; i < NT * 8 * (kD / 8); i += kDecodeThreads) {
+  for (int i = tid; i < NT * 8 * (kD / 8); i += kThreads) {
     const int g = i / (kD / 8), c = i % (kD / 8);
     uint4 raw = make_uint4(0u, 0u, 0u, 0u);
     if (g < p.G) raw = *reinterpret_cast<const uint4*>(p.q + b * p.q_sb + (h0 + g) * p.q_sh + c * 8);
@@ -249,7 +251,7 @@ __global__ void __launch_bounds__(kDecodeThreads) qsa_paged_decode_kernel(const 
     for (int i = 0; i < 16; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
   }
 
-  for (int sub = warp; sub < subs; sub += kDecodeWarps) {
+  for (int sub = warp; sub < subs; sub += kWarps) {
     const uint32_t kbuf = ring + stage * C::kStageBytes, vbuf = kbuf + kSub * C::kPitch;
     const uint32_t mask = stage == 0 ? valid[0] : valid[1];
     cp_async_wait<kStages - 1>();
@@ -383,7 +385,7 @@ __global__ void __launch_bounds__(kDecodeThreads) qsa_paged_decode_kernel(const 
     }
 
     __syncwarp();  // the stage's rows have been read: the next sub-tile may land in it
-    const int next = sub + kStages * kDecodeWarps;
+    const int next = sub + kStages * kWarps;
     if (next < subs) {
       const uint32_t mk = issue(next, stage);
       if (stage == 0) valid[0] = mk; else valid[1] = mk;
@@ -393,7 +395,7 @@ __global__ void __launch_bounds__(kDecodeThreads) qsa_paged_decode_kernel(const 
   }
 
   // ---- merge the warps, then the piece's record or the output ------------------------------
-  __syncthreads();  // both warps are done with the ring and the Q rows
+  __syncthreads();  // all warps are done with the ring and the Q rows
   float* sO = reinterpret_cast<float*>(smem);
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -414,14 +416,14 @@ __global__ void __launch_bounds__(kDecodeThreads) qsa_paged_decode_kernel(const 
     }
   }
   __syncthreads();
-  for (int i = tid; i < p.G * (kD / 4); i += kDecodeThreads) {
+  for (int i = tid; i < p.G * (kD / 4); i += kThreads) {
     const int g = i / (kD / 4), d = (i % (kD / 4)) * 4;
     float top = kNegInf;
 #pragma unroll
-    for (int w = 0; w < kDecodeWarps; ++w) top = fmaxf(top, sState[w][g].x);
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sState[w][g].x);
     float acc[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kDecodeWarps; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
       const float2 st = sState[w][g];
       if (st.x == kNegInf) continue;  // this warp saw no slot
       const float f = fast_exp2(st.x - top);
@@ -535,10 +537,9 @@ DecodePlan decode_plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t P, int32_t pa
   const int G = Hq / Hkv;
   const int resident = kv_fp8 ? (G <= 8 ? Decode<true, 1>::kResident : Decode<true, 2>::kResident)
                               : (G <= 8 ? Decode<false, 1>::kResident : Decode<false, 2>::kResident);
-  // groups of a block per KV head; no more of them than have kMinUnits units when every
-  // sequence is as long as its pages
-  const int64_t cap = (int64_t(P) * page_size + kUnit - 1) / kUnit;
-  const int64_t most = (int64_t(B) * cap + kMinUnits - 1) / kMinUnits;
+  // groups of a block per KV head; no more of them than there are units when every sequence
+  // is as long as its pages
+  const int64_t most = int64_t(B) * ((int64_t(P) * page_size + kUnit - 1) / kUnit);
   int64_t n = (request > 0 ? request : int64_t(num_sms > 0 ? num_sms : 1) * resident) / Hkv;
   n = n > most ? most : n;
   n = n < 1 ? 1 : n;
@@ -572,7 +573,7 @@ cudaError_t launch_decode(const DecodeParams& p, int blocks, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(qsa_paged_decode_kernel<FP8, NT>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::kSmem));
   if (e != cudaSuccess) return e;
-  qsa_paged_decode_kernel<FP8, NT><<<blocks, kDecodeThreads, C::kSmem, st>>>(p);
+  qsa_paged_decode_kernel<FP8, NT><<<blocks, C::kThreads, C::kSmem, st>>>(p);
   return cudaGetLastError();
 }
 

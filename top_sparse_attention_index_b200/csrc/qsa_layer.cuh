@@ -64,22 +64,51 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
   return r;
 }
 
-// int8 codes of eight values over a scale: the value's quotient rounded half to even
-// (IEEE division, so every caller gets the same codes); zeros when the scale is not a
-// positive finite number.
-__device__ __forceinline__ uint2 int8x8_codes(const float (&x)[8], float scale) {
-  uint32_t w[2] = {0u, 0u};
-  if (scale > 0.f && scale < __builtin_huge_valf()) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      w[i >> 2] |= (uint32_t(__float2int_rn(__fdiv_rn(x[i], scale))) & 0xffu) << (8 * (i & 3));
-  }
-  return make_uint2(w[0], w[1]);
+// The scale of int8 codes whose largest magnitude is `top`; NaN when that is not finite.
+__device__ __forceinline__ float code_scale(float top) {
+  const float s = __fdiv_rn(top, 127.f);
+  return s < __builtin_huge_valf() ? s : __int_as_float(0x7fffffff);
 }
 
-// max |x| that keeps a NaN (as NaN).
-__device__ __forceinline__ float nan_max(float a, float b) {
-  return (a != a || b != b) ? __int_as_float(0x7fffffff) : fmaxf(a, b);
+// Largest magnitude of eight values, as the bits of a non-negative float (in whose order a
+// NaN is above infinity); combined across lanes by an unsigned maximum.
+__device__ __forceinline__ uint32_t top_bits(const float (&x)[8]) {
+  uint32_t top = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+  return top;
+}
+
+// int8 codes of eight values over a scale: the 32-bit quotient rounded half to even, so every
+// caller gets the same codes; zeros when the scale is not a positive finite number.  The
+// product with the reciprocal is within 127 * 3 * 2^-24 of the quotient (at most 127 in
+// magnitude), so it rounds to the same code unless it lies that close to a half: only then
+// are the quotients themselves taken (also when the reciprocal of a tiny scale overflows).
+// Adding 1.5 * 2^23 rounds to a whole number and leaves it in the low bits.
+__device__ __forceinline__ uint2 int8x8_codes(const float (&x)[8], float scale) {
+  if (!(scale > 0.f && scale < __builtin_huge_valf())) return make_uint2(0u, 0u);
+  const float inv = __frcp_rn(scale);
+  uint32_t c[8];
+  bool close = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float q = __fmul_rn(x[i], inv), t = __fadd_rn(q, 12582912.f);
+    close |= !(fabsf(q - __fsub_rn(t, 12582912.f)) < 0.5f - 0x1p-13f);
+    c[i] = __float_as_uint(t);
+  }
+  if (close) {
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      float v = x[0];  // x[i], without an index into registers
+#pragma unroll
+      for (int k = 1; k < 8; ++k) v = i == k ? x[k] : v;
+      const uint32_t q = __float_as_uint(__fadd_rn(__fdiv_rn(v, scale), 12582912.f));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) c[k] = i == k ? q : c[k];
+    }
+  }
+  return make_uint2(byte_perm(byte_perm(c[0], c[1], 0x0040u), byte_perm(c[2], c[3], 0x0040u), 0x5410u),
+                    byte_perm(byte_perm(c[4], c[5], 0x0040u), byte_perm(c[6], c[7], 0x0040u), 0x5410u));
 }
 
 __device__ __forceinline__ uint64_t clock_ns() {

@@ -7,8 +7,8 @@ namespace {
 
 using namespace qsa;
 
-constexpr int kMaxPairs = 128;  // rot / 2 at D = 256
-constexpr int kRopeRows = 4;    // warp-rows in flight per warp
+constexpr int kMaxPairs = 128;    // rot / 2 at D = 256
+constexpr int kRopeWarps = 4;     // of a thread block; each works for itself
 
 struct RopeParams {
   const uint16_t *q, *k, *v, *qw, *kw;
@@ -20,134 +20,208 @@ struct RopeParams {
   uint8_t *k_dst, *v_dst;
   int64_t qo_st, qo_sh, kd_ss, kd_sh, vd_ss, vd_sh;  // kd, vd: bytes
   const int32_t* slots;
-  int64_t rows;
+  int64_t rows, units;  // units: T * parts
   uint32_t* err_word;
   int32_t T, Hq, Hkv, half, interleaved;
+  int32_t q_steps, k_steps, v_steps, steps, parts;  // of a token; of a warp; warps of a token
   int32_t axis_end[QSA_MAX_ROPE_AXES];  // pairs below axis_end[a] (and not below a - 1's) turn by a
-  float offset, eps, rope_scale, k_scale, v_scale;
+  float offset, eps, rope_scale, inv_k_scale, inv_v_scale;
   int32_t kv_fp8;
 };
 
-// One thread block per token; a row (one head of q, k or v) is D / 8 lanes of 16 bytes, so
-// a warp holds 256 / D rows, and each warp keeps kRopeRows of them in flight.  Every byte
-// is read and written once: the bound is HBM.  The token's sines and cosines are made once
-// per block (one pair per thread) and shared by its heads: made per row they would cost
-// more instructions than the row's own work.  The pair of dimension d in the halves form
-// is d +- rot / 2, which another lane of the row holds at the same place of its vector
-// (rot / 2 is a multiple of 8): one shuffle per element.
+__device__ __forceinline__ void bf16x8_to_pairs(const uint4& r, uint64_t (&x)[4]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = pack2(bf16lo_to_f32(w[i]), bf16hi_to_f32(w[i]));
+}
+
+__device__ __forceinline__ uint4 pairs_to_bf16x8(const uint64_t (&x)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    unpack2(x[i], lo, hi);
+    w[i] = pack_bf16x2(lo, hi);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ uint2 pairs_to_e4m3x8(const uint64_t (&x)[4], uint64_t inv) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    unpack2(mul2(x[i], inv), lo, hi);
+    w[i] = pack_e4m3x2(lo, hi);
+  }
+  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+// A warp takes `steps` steps of one token, a step being 512 / D rows of q, of k or of v: every
+// warp makes its token's sines and cosines for itself.  A row is D / 16 lanes of two 16-byte
+// vectors, chosen so that both dimensions of every rotated pair are in one lane (halves:
+// vectors l and l + rot / 16 for the rotated part; otherwise neighbours), so the rotation
+// crosses no lanes and a lane's eight (cos, sin) and its weights stay in registers for all
+// its rows; two values per arithmetic instruction; a step loads while the last is worked on.
+// Bound: every byte is read and written once, HBM.
 template <int D>
-__global__ void qsa_norm_rope_kernel(const RopeParams p) {
-  constexpr int kLanes = D / 8;        // lanes of a row
-  constexpr int kPer = 32 / kLanes;    // rows of a warp access
-  __shared__ float2 sTurn[kMaxPairs];  // (cos, sin) of the token's pairs
-  const int t = blockIdx.x;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+__global__ void __launch_bounds__(32 * kRopeWarps, 5) qsa_norm_rope_kernel(const RopeParams p) {
+  constexpr int kLanes = D / 16;      // lanes of a row
+  constexpr int kRows = 32 / kLanes;  // rows of a step
+  __shared__ float2 sTurn[kRopeWarps][kMaxPairs];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t unit = int64_t(blockIdx.x) * kRopeWarps + warp;
+  if (unit >= p.units) return;
+  const int t = p.parts == 1 ? int(unit) : int(unit / p.parts);
+  const int first = int(unit - int64_t(t) * p.parts) * p.steps;
+  const int all = p.q_steps + p.k_steps + p.v_steps, end = min(first + p.steps, all);
+
   const int sub = lane / kLanes, l = lane % kLanes;
-  const int n_k = p.k != nullptr ? p.Hkv : 0, n_v = p.v != nullptr ? p.Hkv : 0;
-  const int n_rows = p.Hq + n_k + n_v;
+  const int turned = p.interleaved ? 0 : p.half >> 3;  // lanes whose vectors are a half apart
+  const int va = l < turned ? l : 2 * l, vb = l < turned ? l + turned : 2 * l + 1;
+  auto kind_of = [&](int step) { return step < p.q_steps ? 0 : step < p.q_steps + p.k_steps ? 1 : 2; };  // q, k, v
+  auto head_of = [&](int step, int kind) {
+    return (step - (kind == 0 ? 0 : kind == 1 ? p.q_steps : p.q_steps + p.k_steps)) * kRows + sub;
+  };
+  // the next step's rows: this lane's row of it, rows of the kind that are left from it on, and
+  // the kind's pitch between steps
+  uint4 raw[2], next[2];
+  const uint16_t* row_in = nullptr;
+  int64_t pitch_in = 0;
+  int left_in = 0, kind_in = -1;
+  auto load = [&](int step) {
+    if (kind_of(step) != kind_in) {
+      kind_in = kind_of(step);
+      const int h = head_of(step, kind_in);
+      const int64_t sh = kind_in == 0 ? p.q_sh : kind_in == 1 ? p.k_sh : p.v_sh;
+      row_in = (kind_in == 0 ? p.q + t * p.q_st : kind_in == 1 ? p.k + t * p.k_st : p.v + t * p.v_st) + h * sh;
+      pitch_in = sh * kRows;
+      left_in = (kind_in == 0 ? p.Hq : p.Hkv) - h;
+    }
+    next[0] = next[1] = make_uint4(0u, 0u, 0u, 0u);
+    if (left_in > 0) {
+      next[0] = *reinterpret_cast<const uint4*>(row_in + va * 8);
+      next[1] = *reinterpret_cast<const uint4*>(row_in + vb * 8);
+    }
+    row_in += pitch_in;
+    left_in -= kRows;
+  };
+  load(first);
 
   int64_t dst = t;
-  if (p.slots != nullptr) {
+  if (end > p.q_steps && p.slots != nullptr) {
     const int32_t s = p.slots[t];
+    dst = s;
     if (s < -1 || s >= p.rows) {
-      if (threadIdx.x == 0 && p.err_word != nullptr) atomicOr(p.err_word, QSA_ERRBIT_SLOT_RANGE);
+      if (lane == 0 && p.err_word != nullptr) atomicOr(p.err_word, QSA_ERRBIT_SLOT_RANGE);
       dst = -1;
-    } else {
-      dst = s;
     }
   }
+  if (p.half > 0 && first < p.q_steps + p.k_steps) {
+    for (int i = lane; i < p.half; i += 32) {
+      int a = 0;
+      while (i >= p.axis_end[a]) ++a;  // axis_end[axes - 1] = half
+      // the angle in whole turns, reduced in 64 bits: position * inv_freq has up to 55 bits
+      const double turns = double(p.pos[a * p.pos_stride + t]) * double(p.inv_freq[i]) *
+                           0.15915494309189533576888;  // 1 / (2 pi)
+      float s, c;
+      sincospif(2.0f * float(turns - rint(turns)), &s, &c);
+      sTurn[warp][i] = make_float2(c * p.rope_scale, s * p.rope_scale);
+    }
+    __syncwarp();
+  }
+  // this lane's pairs: halves, pair 8 va + e is (a[e], b[e]); neighbours, pair 4 va + e is
+  // (a[2 e], a[2 e + 1]) and pair 4 vb + e is (b[2 e], b[2 e + 1])
+  const bool turns_a = p.interleaved ? va * 4 < p.half : l < turned;
+  const bool turns_b = p.interleaved && vb * 4 < p.half;
+  float c[8], s[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int i = !p.interleaved ? va * 8 + e : e < 4 ? va * 4 + e : vb * 4 + e - 4;
+    const float2 cs = turns_a && i < p.half ? sTurn[warp][i] : make_float2(1.f, 0.f);
+    c[e] = cs.x;
+    s[e] = cs.y;
+  }
 
-  for (int r0 = warp * kPer * kRopeRows; r0 < n_rows || r0 == warp * kPer * kRopeRows;
-       r0 += warps * kPer * kRopeRows) {
-    uint4 raw[kRopeRows];
+  int kind = -1, left = 0;
+  const uint16_t* w = nullptr;
+  uint8_t* row = nullptr;
+  int64_t pitch = 0;
+  uint64_t wa[4], wb[4];
+  for (int step = first; step < end; ++step) {
+    raw[0] = next[0], raw[1] = next[1];
+    if (step + 1 < end) load(step + 1);
+    if (kind_of(step) != kind) {  // the weights and destinations of this kind of rows
+      kind = kind_of(step);
+      const int h = head_of(step, kind);
+      const int64_t sh = kind == 0 ? p.qo_sh * 2 : kind == 1 ? p.kd_sh : p.vd_sh;
+      row = (kind == 0   ? reinterpret_cast<uint8_t*>(p.q_out + t * p.qo_st)
+             : kind == 1 ? p.k_dst + dst * p.kd_ss
+                         : p.v_dst + dst * p.vd_ss) + h * sh;
+      pitch = sh * kRows;
+      left = kind == 0 ? p.Hq - h : dst >= 0 ? p.Hkv - h : 0;
+      w = kind == 0 ? p.qw : kind == 1 ? p.kw : nullptr;
+      if (w != nullptr) {
+        const uint64_t offset2 = pack2(p.offset, p.offset);
+        bf16x8_to_pairs(__ldg(reinterpret_cast<const uint4*>(w + va * 8)), wa);
+        bf16x8_to_pairs(__ldg(reinterpret_cast<const uint4*>(w + vb * 8)), wb);
 #pragma unroll
-    for (int i = 0; i < kRopeRows; ++i) {
-      const int r = r0 + i * kPer + sub;
-      raw[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < n_rows) {
-        const uint16_t* src = r < p.Hq ? p.q + t * p.q_st + r * p.q_sh
-                              : r < p.Hq + n_k ? p.k + t * p.k_st + (r - p.Hq) * p.k_sh
-                                               : p.v + t * p.v_st + (r - p.Hq - n_k) * p.v_sh;
-        raw[i] = *reinterpret_cast<const uint4*>(src + l * 8);
+        for (int e = 0; e < 4; ++e) wa[e] = add2(wa[e], offset2), wb[e] = add2(wb[e], offset2);
       }
     }
-    if (r0 == warp * kPer * kRopeRows) {  // the block's first round: make the turns
-      for (int i = threadIdx.x; i < p.half; i += blockDim.x) {
-        int a = 0;
-        while (i >= p.axis_end[a]) ++a;  // axis_end[axes - 1] = half
-        // the angle in whole turns, reduced in 64 bits: position * inv_freq has up to 55 bits
-        const double turns = double(p.pos[a * p.pos_stride + t]) * double(p.inv_freq[i]) *
-                             0.15915494309189533576888;  // 1 / (2 pi)
-        float s, c;
-        sincospif(2.0f * float(turns - rint(turns)), &s, &c);
-        sTurn[i] = make_float2(c * p.rope_scale, s * p.rope_scale);
-      }
-      __syncthreads();
-    }
+    uint64_t a[4], b[4];
+    bf16x8_to_pairs(raw[0], a);
+    bf16x8_to_pairs(raw[1], b);
+    if (w != nullptr) {
+      uint64_t sq = mul2(a[0], a[0]), sq2 = mul2(b[0], b[0]);
 #pragma unroll
-    for (int i = 0; i < kRopeRows; ++i) {
-      const int r = r0 + i * kPer + sub;
-      if (r0 + i * kPer >= n_rows) break;  // whole warp past the end
-      const bool is_q = r < p.Hq, is_k = !is_q && r < p.Hq + n_k;
-      float x[8];
-      bf16x8_to_f32(raw[i], x);
-      const uint16_t* w = is_q ? p.qw : is_k ? p.kw : nullptr;
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+      for (int e = 1; e < 4; ++e) sq = fma2(a[e], a[e], sq), sq2 = fma2(b[e], b[e], sq2);
+      float ss, hi;
+      unpack2(add2(sq, sq2), ss, hi);
+      ss += hi;
 #pragma unroll
       for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (w != nullptr) {
-        const float inv = 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
-        float wf[8];
-        bf16x8_to_f32(*reinterpret_cast<const uint4*>(w + l * 8), wf);
+      const float inv = rsqrtf(ss * (1.0f / D) + p.eps);
+      const uint64_t inv2 = pack2(inv, inv);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * (wf[e] + p.offset);
+      for (int e = 0; e < 4; ++e) {
+        a[e] = mul2(mul2(a[e], inv2), wa[e]);
+        b[e] = mul2(mul2(b[e], inv2), wb[e]);
       }
-      // the shuffles below run for every lane; rows of v and lanes past rot keep x
-      const bool turn = (is_q || is_k) && l * 8 < 2 * p.half;
+    }
+    if (kind != 2) {
       if (p.interleaved) {
-        if (turn) {
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const float2 cs = sTurn[l * 4 + (e >> 1)];
-            const float u = x[e], v = x[e + 1];
-            x[e] = u * cs.x - v * cs.y;
-            x[e + 1] = v * cs.x + u * cs.y;
-          }
+        for (int e = 0; e < 4; ++e) {
+          float u, v;
+          unpack2(a[e], u, v);
+          if (turns_a) a[e] = pack2(u * c[e] - v * s[e], v * c[e] + u * s[e]);
+          unpack2(b[e], u, v);
+          if (turns_b) b[e] = pack2(u * c[4 + e] - v * s[4 + e], v * c[4 + e] + u * s[4 + e]);
         }
-      } else if (p.half > 0) {
-        const int hl = p.half >> 3;  // lanes of half the rotated part
-        const bool low = l < hl;
-        const int other = sub * kLanes + (turn ? (low ? l + hl : l - hl) : l);
-        const int pair0 = low ? l * 8 : l * 8 - p.half;
+      } else if (turns_a) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float y = __shfl_sync(0xffffffffu, x[e], other);
-          if (turn) {
-            const float2 cs = sTurn[pair0 + e];
-            x[e] = low ? x[e] * cs.x - y * cs.y : x[e] * cs.x + y * cs.y;
-          }
-        }
-      }
-      if (r >= n_rows) continue;
-      if (is_q) {
-        *reinterpret_cast<uint4*>(p.q_out + t * p.qo_st + r * p.qo_sh + l * 8) = f32_to_bf16x8(x);
-      } else if (dst >= 0) {
-        const int h = is_k ? r - p.Hq : r - p.Hq - n_k;
-        uint8_t* row = is_k ? p.k_dst + dst * p.kd_ss + h * p.kd_sh : p.v_dst + dst * p.vd_ss + h * p.vd_sh;
-        if (p.kv_fp8) {
-          const float sc = is_k ? p.k_scale : p.v_scale;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = __fdiv_rn(x[e], sc);
-          *reinterpret_cast<uint2*>(row + l * 8) =
-              make_uint2(pack_e4m3x2(x[0], x[1]) | (pack_e4m3x2(x[2], x[3]) << 16),
-                         pack_e4m3x2(x[4], x[5]) | (pack_e4m3x2(x[6], x[7]) << 16));
-        } else {
-          *reinterpret_cast<uint4*>(row + l * 16) = f32_to_bf16x8(x);
+        for (int e = 0; e < 4; ++e) {
+          const uint64_t c2 = pack2(c[2 * e], c[2 * e + 1]), s2 = pack2(s[2 * e], s[2 * e + 1]);
+          const uint64_t n2 = pack2(-s[2 * e], -s[2 * e + 1]), u = a[e];
+          a[e] = fma2(u, c2, mul2(b[e], n2));
+          b[e] = fma2(b[e], c2, mul2(u, s2));
         }
       }
     }
+    if (left > 0) {
+      if (kind != 0 && p.kv_fp8) {
+        const float scale = kind == 1 ? p.inv_k_scale : p.inv_v_scale;
+        const uint64_t scale2 = pack2(scale, scale);
+        *reinterpret_cast<uint2*>(row + va * 8) = pairs_to_e4m3x8(a, scale2);
+        *reinterpret_cast<uint2*>(row + vb * 8) = pairs_to_e4m3x8(b, scale2);
+      } else {
+        *reinterpret_cast<uint4*>(row + va * 16) = pairs_to_bf16x8(a);
+        *reinterpret_cast<uint4*>(row + vb * 16) = pairs_to_bf16x8(b);
+      }
+    }
+    row += pitch;
+    left -= kRows;
   }
 }
 
@@ -165,10 +239,11 @@ struct PackParams {
 
 // Di / 8 lanes per micro-block, each summing its eight dimensions over the block's slots
 // in order; the maximum crosses the lanes by shuffles.  HBM-bound: the keys are read once.
+constexpr int kPackThreads = 128;
 template <int DI>
-__global__ void __launch_bounds__(256) qsa_pack_index_kernel(const PackParams p) {
+__global__ void __launch_bounds__(kPackThreads) qsa_pack_index_kernel(const PackParams p) {
   constexpr int kLanes = DI / 8;
-  const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) / kLanes;
+  const int64_t i = (int64_t(blockIdx.x) * kPackThreads + threadIdx.x) / kLanes;
   const int l = threadIdx.x % kLanes;
   int64_t b = -1;
   if (i < p.n) {
@@ -178,7 +253,7 @@ __global__ void __launch_bounds__(256) qsa_pack_index_kernel(const PackParams p)
       b = -1;
     }
   }
-  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  uint64_t sum2[4] = {0u, 0u, 0u, 0u};  // two sums each
   if (b >= 0) {
     const uint16_t* src = p.keys + b * p.block * p.key_stride + l * 8;
     for (int e0 = 0; e0 < p.block; e0 += 4) {
@@ -189,24 +264,31 @@ __global__ void __launch_bounds__(256) qsa_pack_index_kernel(const PackParams p)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (e0 + e >= p.block) break;
-        float x[8];
-        bf16x8_to_f32(raw[e], x);
+        uint64_t x[4];
+        bf16x8_to_pairs(raw[e], x);
 #pragma unroll
-        for (int d = 0; d < 8; ++d) sum[d] = e0 + e == 0 ? x[d] : __fadd_rn(sum[d], x[d]);
+        for (int d = 0; d < 4; ++d) sum2[d] = e0 + e == 0 ? x[d] : add2(sum2[d], x[d]);
       }
     }
   }
-  float top = 0.f;
+  float sum[8];
+  if ((p.block & (p.block - 1)) == 0) {  // the product with a power of two's reciprocal is the quotient
+    const float inv = 1.0f / float(p.block);
 #pragma unroll
-  for (int d = 0; d < 8; ++d) {
-    sum[d] = __fdiv_rn(sum[d], float(p.block));
-    top = nan_max(top, fabsf(sum[d]));
+    for (int d = 0; d < 4; ++d) unpack2(mul2(sum2[d], pack2(inv, inv)), sum[2 * d], sum[2 * d + 1]);
+  } else {
+#pragma unroll
+    for (int d = 0; d < 8; ++d) {
+      float x[2];
+      unpack2(sum2[d >> 1], x[0], x[1]);
+      sum[d] = __fdiv_rn(x[d & 1], float(p.block));
+    }
   }
+  uint32_t top = top_bits(sum);
 #pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) top = nan_max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
   if (b < 0) return;
-  float scale = __fdiv_rn(top, 127.f);
-  if (!(scale < __builtin_huge_valf())) scale = __int_as_float(0x7fffffff);
+  const float scale = code_scale(__uint_as_float(top));
   *reinterpret_cast<uint2*>(p.codes + b * p.code_stride + l * 8) = int8x8_codes(sum, scale);
   if (l == 0) p.scales[b] = scale;
 }
@@ -237,8 +319,9 @@ extern "C" qsa_status_t qsa_qk_norm_rope(
   if (kv_fp8 != 0 && kv_fp8 != 1) QSA_REJECT(QSA_ERR_INVALID_ARG, "kv_fp8 must be 0 or 1");
   if (!std::isfinite(weight_offset) || !std::isfinite(eps) || eps < 0.f || !std::isfinite(rope_scale))
     QSA_REJECT(QSA_ERR_INVALID_ARG, "weight_offset, eps (>= 0) and rope_scale must be finite");
-  if (kv_fp8 && !(k_scale > 0.f && std::isfinite(k_scale) && v_scale > 0.f && std::isfinite(v_scale)))
-    QSA_REJECT(QSA_ERR_INVALID_ARG, "k_scale and v_scale must be positive and finite");
+  if (kv_fp8 && !(k_scale > 0.f && std::isfinite(1.0f / k_scale) && std::isfinite(k_scale) && v_scale > 0.f &&
+                  std::isfinite(1.0f / v_scale) && std::isfinite(v_scale)))
+    QSA_REJECT(QSA_ERR_INVALID_ARG, "k_scale and v_scale must be positive and finite, and so their reciprocals");
   RopeParams p{};
   p.half = rot / 2;
   if (sections == nullptr) {
@@ -301,15 +384,25 @@ extern "C" qsa_status_t qsa_qk_norm_rope(
   p.err_word = err_word;
   p.T = T, p.Hq = Hq, p.Hkv = Hkv, p.interleaved = interleaved;
   p.offset = weight_offset, p.eps = eps, p.rope_scale = rope_scale;
-  p.k_scale = k_scale, p.v_scale = v_scale, p.kv_fp8 = kv_fp8;
-  const int n_rows = Hq + (k != nullptr ? Hkv : 0) + (v != nullptr ? Hkv : 0);
-  const int per_warp = 256 / D * kRopeRows;
-  int warps = (n_rows + per_warp - 1) / per_warp;
-  warps = warps > 16 ? 16 : warps;
+  p.inv_k_scale = 1.0f / k_scale, p.inv_v_scale = 1.0f / v_scale, p.kv_fp8 = kv_fp8;
+  // A warp takes a whole token once that gives every SM some 32 warps, else as many steps as
+  // do, at least two (it makes its token's sines and cosines, about the work of three steps).
+  const int per_step = 512 / D;
+  p.q_steps = (Hq + per_step - 1) / per_step;
+  p.k_steps = k != nullptr ? (Hkv + per_step - 1) / per_step : 0;
+  p.v_steps = v != nullptr ? (Hkv + per_step - 1) / per_step : 0;
+  const int64_t all = p.q_steps + p.k_steps + p.v_steps;
+  int64_t steps = (int64_t(T) * all + 148 * 32 - 1) / (148 * 32);
+  steps = steps < 2 ? 2 : steps;
+  p.parts = int32_t((all + steps - 1) / steps);
+  p.steps = int32_t((all + p.parts - 1) / p.parts);
+  p.units = int64_t(T) * p.parts;
+  const int64_t grid = (p.units + kRopeWarps - 1) / kRopeWarps;
+  if (grid > INT32_MAX) QSA_REJECT(QSA_ERR_UNSUPPORTED, "%lld thread blocks in one launch", (long long)grid);
   const auto st = static_cast<cudaStream_t>(stream);
-  if (D == 256) qsa_norm_rope_kernel<256><<<T, warps * 32, 0, st>>>(p);
-  else if (D == 128) qsa_norm_rope_kernel<128><<<T, warps * 32, 0, st>>>(p);
-  else qsa_norm_rope_kernel<64><<<T, warps * 32, 0, st>>>(p);
+  if (D == 256) qsa_norm_rope_kernel<256><<<unsigned(grid), 32 * kRopeWarps, 0, st>>>(p);
+  else if (D == 128) qsa_norm_rope_kernel<128><<<unsigned(grid), 32 * kRopeWarps, 0, st>>>(p);
+  else qsa_norm_rope_kernel<64><<<unsigned(grid), 32 * kRopeWarps, 0, st>>>(p);
   return launch_status(cudaGetLastError(), "qsa_qk_norm_rope");
 }
 
@@ -342,10 +435,10 @@ extern "C" qsa_status_t qsa_pack_index_keys(const void* keys, int64_t key_stride
   p.n_blocks = S / block;
   p.n = n;
   p.block = block;
-  const int per = 256 / (Di / 8);
+  const int per = kPackThreads / (Di / 8);
   const int grid = int((int64_t(n) + per - 1) / per);
   const auto st = static_cast<cudaStream_t>(stream);
-  if (Di == 128) qsa_pack_index_kernel<128><<<grid, 256, 0, st>>>(p);
-  else qsa_pack_index_kernel<64><<<grid, 256, 0, st>>>(p);
+  if (Di == 128) qsa_pack_index_kernel<128><<<grid, kPackThreads, 0, st>>>(p);
+  else qsa_pack_index_kernel<64><<<grid, kPackThreads, 0, st>>>(p);
   return launch_status(cudaGetLastError(), "qsa_pack_index_keys");
 }

@@ -195,14 +195,12 @@ __global__ void __launch_bounds__(kScoreThreads) qsa_select_score_kernel(const S
       uint4 raw = make_uint4(0u, 0u, 0u, 0u);
       if (live)
         raw = *reinterpret_cast<const uint4*>(p.q + (t0 + row) * p.q_st + head * p.q_sh + l * 8);
-      float xs[8], top = 0.f;
+      float xs[8];
       bf16x8_to_f32(raw, xs);
+      uint32_t top = top_bits(xs);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top = nan_max(top, fabsf(xs[e]));
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) top = nan_max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      float scale = __fdiv_rn(top, 127.f);
-      if (!(scale < __builtin_huge_valf())) scale = __int_as_float(0x7fffffff);
+      for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float scale = code_scale(__uint_as_float(top));
       *reinterpret_cast<uint2*>(sQ + v * DI + (swz(c, l >> 1) << 4) + (l & 1) * 8) = int8x8_codes(xs, scale);
       if (l == 0) sGain[v] = live ? __fmul_rn(p.weight[(t0 + row) * p.w_st + head], scale) : 0.f;
     }
@@ -357,14 +355,12 @@ __global__ void __launch_bounds__(256) qsa_select_prep_kernel(const SelectParams
     for (int u = 0; u < kAhead; ++u) {
       const int v = ((i0 + u) * 8 + warp) * kVec + lane / kLanes;
       const int row = v / (2 * HP) * 2 + (v & 1), head = (v % (2 * HP)) >> 1;
-      float xs[8], top = 0.f;
+      float xs[8];
       bf16x8_to_f32(raw[u], xs);
+      uint32_t top = top_bits(xs);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top = nan_max(top, fabsf(xs[e]));
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) top = nan_max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      float scale = __fdiv_rn(top, 127.f);
-      if (!(scale < __builtin_huge_valf())) scale = __int_as_float(0x7fffffff);
+      for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float scale = code_scale(__uint_as_float(top));
       const int c = l >> 1;
       *reinterpret_cast<uint2*>(dst + (c >> 1) * (kWideCols * 32) + (v >> 3) * 256 + (c & 1) * 128 + (v & 7) * 16 +
                                 (l & 1) * 8) = int8x8_codes(xs, scale);
