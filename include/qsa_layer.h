@@ -127,8 +127,8 @@ qsa_status_t qsa_pack_index_keys(const void* keys, int64_t key_stride_s, const i
  *   page_table  int32 [B, P], row stride page_stride: the sequence's tokens
  *               [page_size m, page_size (m + 1)) lie in the slots of page page_table[b, m].
  *               page_size is a multiple of block.  A page outside [0, pages) sets
- *               QSA_ERRBIT_SLOT_RANGE; its blocks score below all others and its slots
- *               come out as -1.
+ *               QSA_ERRBIT_SLOT_RANGE; its blocks score -infinity and its slots come out
+ *               as -1.
  *   seq_lens    int32 [B]; values outside [0, P page_size] are clamped and set
  *               QSA_ERRBIT_WIDTH_RANGE, as do values of cu_q outside [0, Tq].
  *   1 <= Hi <= 64, Di 64 or 128, block 1..16, top_blocks >= 1 with top_blocks * block <= 8192,

@@ -103,8 +103,8 @@ def select(q, weight, codes, scales, table, lens, cu, top, page, block, sink, lo
                 for h in range(1, Hi):
                     s = (s + (gain[h] * dots[h]).astype(np.float32)).astype(np.float32)
                 s = (s * scales[phys]).astype(np.float64)
-            s[np.isnan(s)] = -np.inf
-            rank = np.where((j < sink) | (j >= f - local), 0, np.where(ok, 1, 2))
+            s[np.isnan(s) | ~ok] = -np.inf
+            rank = np.where((j < sink) | (j >= f - local), 0, 1)
             order = np.lexsort((j, -s, rank))[:top]
             row = []
             for k in sorted(order):

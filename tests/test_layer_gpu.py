@@ -675,3 +675,36 @@ def test_select_order_of_a_long_row(kind, rows):
             want, want_width = ref.select(one["q"], one["weight"], c["codes"], c["scales"], c["page_table"],
                                           one["seq_lens"], None, top, c["page_size"], 1, sink, local)
             assert torch.equal(got[t].cpu(), torch.from_numpy(want[0])) and int(width[t]) == int(want_width[0])
+
+
+@pytest.mark.parametrize("n", [130, 1000, 2000])
+@pytest.mark.parametrize("kind", ["random", "falling", "two_values", "equal", "spread", "few_best"])
+def test_select_order_of_many_short_rows(kind, n):
+    """More rows than two per SM, none longer than 2,048 blocks."""
+    x = torch.rand(n, generator=gen(92), device="cuda") + 0.5
+    if kind == "falling":
+        x = x.sort(descending=True).values
+    elif kind == "two_values":
+        x = torch.where(x > 1.2, 2.0, 1.0)
+    elif kind == "equal":
+        x.fill_(1.0)
+    elif kind == "spread":
+        x = torch.exp2((x - 1) * 250)
+    elif kind == "few_best":
+        x[n // 2:n // 2 + 5] += 1000
+    rows = 420
+    c = keyed_case(x, rows, 0)
+    for top, sink, local in ((100, 0, 0), (100, 1, 7), (1, 0, 0), (129, 100, 29), (500, 0, 3)):
+        got, width = run_select(c, top, sink, local)
+        for t in (0, 1, 2, 3, rows // 2, rows - 2, rows - 1):
+            want, want_width = ref.select(c["q"][t:t + 1], c["weight"][t:t + 1], c["codes"], c["scales"], c["page_table"],
+                                          c["seq_lens"] - (rows - 1 - t), None, top, c["page_size"], 1, sink, local)
+            assert torch.equal(got[t].cpu(), torch.from_numpy(want[0])) and int(width[t]) == int(want_width[0])
+
+
+def test_select_many_short_rows_of_several_sequences():
+    c = select_case(93, [900, 3, 2003, 1500], [200, 3, 150, 70], 4, 128, 4, 64, gap=2)
+    assert check_select(c, 40, 1, 3) == 0
+    c["page_table"][2, 5], c["scales"][::3] = -1, float("nan")
+    assert check_select(c, 40) == SLOT_RANGE
+    assert check_select(c, 300) == SLOT_RANGE

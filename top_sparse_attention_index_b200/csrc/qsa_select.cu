@@ -12,8 +12,9 @@ namespace {
 
 using namespace qsa;
 
-constexpr int kKeyTile = 128;                 // micro-blocks per tile: 16 per warp
+constexpr int kKeyTile = 128;                 // micro-blocks per tile
 constexpr int kScoreThreads = 256;
+constexpr int kScoreBlocks = 2;               // of an SM
 constexpr int64_t kChunkBytes = 64 << 20;     // keys of one chunk of rows
 constexpr int kMinChunkRows = 64;
 
@@ -24,7 +25,7 @@ struct SelectParams {
   const float* scales;
   const int32_t *table, *lens, *cu;
   int32_t *out, *width;
-  uint32_t* keys;      // [chunk rows, ld]
+  float* scores;       // [chunk rows, ld]
   uint32_t* err_word;
   int64_t q_st, q_sh, w_st, code_st, table_st, out_st, pages, ld;
   int32_t c0, c1;      // the chunk's rows
@@ -33,16 +34,23 @@ struct SelectParams {
   uint8_t* tile_q;
   int32_t cap, window;              // keys of a row, and words of its marks, in the choice's shared memory
   uint32_t page_magic, block_magic; // 2^32 / per_page (/ block), rounded up
-  int32_t chunk_tiles, chunks;  // score kernel: key tiles of a thread block, blocks of a row tile
 };
 
-// The order of floats as an order of unsigned integers; NaN and -infinity share the lowest
-// value a block can have, -0 equals +0.  0 is left for blocks of a page outside the pool,
-// 0xffffffff for blocks that are taken whatever they score.
-__device__ __forceinline__ uint32_t order_key(float s) {
-  s = s != s ? -__builtin_huge_valf() : s + 0.0f;
-  const uint32_t u = __float_as_uint(s);
-  return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+// The score as it is kept: a NaN (of the codes or weights, or the scale of a block whose page
+// lies outside the pool) counts as -infinity, -0 as +0.
+__device__ __forceinline__ float kept_score(float sum, float scale) {
+  return fmaxf(__fmaf_rn(sum, scale, 0.f), -__builtin_huge_valf());
+}
+
+// The order of scores as an order of unsigned integers, -infinity at kLeastKey; 0 is left for
+// blocks that take no part.  And back.
+constexpr uint32_t kLeastKey = 0x007fffffu;
+__device__ __forceinline__ uint32_t order_key(uint32_t score) {
+  return score ^ (uint32_t(int32_t(score) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float key_score(uint32_t key) {
+  key = max(key, kLeastKey);
+  return __uint_as_float((key >> 31) ? key ^ 0x80000000u : ~key);
 }
 
 // Rows of sequence b, clamped to [0, Tq].
@@ -85,183 +93,241 @@ __device__ __forceinline__ int block_scan(int v, int* tmp, int& total) {
   return v + before;
 }
 
-// ---- the score ---------------------------------------------------------------------------
+// ---- the score of few rows per sequence -----------------------------------------------------
 
-// Columns of a tile: 8 NT of them, a thread of quad position u holding columns 2u and 2u + 1
-// of every n8 tile: kPer = 2 NT columns, which are kPer / HP rows of HP heads each, so one
-// thread holds all heads of a row (16 at a time) and adds them in order without crossing
+// Columns of a tile of rows: 8 NT of them, a thread of quad position u holding columns 2u and
+// 2u + 1 of every n8 tile: kPer = 2 NT columns, which are kPer / HP rows of HP heads each, so
+// one thread holds all heads of a row (16 at a time) and adds them in order without crossing
 // lanes.  Column c of an n8 tile i is (row u kPer/HP + x / HP, head x mod HP) with u = c / 2
 // and x = 2 i + (c mod 2).  Heads beyond Hi, and rows beyond the tile's, have gain 0.
 template <int DI, int HP, int NT>
 struct Score {
-  static constexpr int kCols = 8 * NT;
   static constexpr int kPer = 2 * NT;       // columns of a thread
   static constexpr int kRx = kPer / HP;     // rows of a thread
   static constexpr int kRows = 4 * kRx;     // rows of a tile
-  static constexpr int kTileBytes = kKeyTile * DI;
+  static constexpr int kSteps = DI / 32;    // k-steps of a product
   static_assert(kPer % HP == 0 && kRx >= 1, "a thread holds whole rows");
-  // two key tiles, the query codes and gains, and per key tile the scales and valid marks
-  static size_t smem(int groups) {
-    return 2 * kTileBytes + size_t(groups) * kCols * (DI + 4) + 4 * kKeyTile * 4;
-  }
+  // the query codes as the MMA's B fragments, and the gains
+  static size_t smem(int groups) { return size_t(groups) * NT * (kSteps * 256 + 32); }
 };
 
+// The units (128 blocks of one tile of rows) of all sequences are shared out evenly over the
+// thread blocks; the eight warps of one take 16 blocks of a unit each.  A lane holds, of two
+// of the 16 blocks, 16 bytes of every 64 as they lie in memory: that is an A fragment of the
+// 8-bit MMA up to the order of the products in the sum, which is exact, and the query codes
+// are put in the same order; so the codes go from memory to the MMA without shared memory,
+// the next blocks' loads in flight, and the page lookups one step further ahead.
+// Bound: HBM, the codes are read once per four rows or more of a sequence.
+// (128-block tiles through shared memory with a barrier each, split evenly by the page table's
+// capacity, took 44 us for 64 rows over ragged caches of up to 16,384 blocks.)
 template <int DI, int HP, int NT>
-__global__ void __launch_bounds__(kScoreThreads) qsa_select_score_kernel(const SelectParams p, int groups) {
+__global__ void __launch_bounds__(kScoreThreads, kScoreBlocks)
+    qsa_select_score_kernel(const SelectParams p, int groups) {
   using C = Score<DI, HP, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
-  uint8_t* sQ = smem + 2 * C::kTileBytes;
-  float* sGain = reinterpret_cast<float*>(sQ + groups * C::kCols * DI);
-  float* sScale = sGain + groups * C::kCols;                     // [2][kKeyTile]
-  int* sValid = reinterpret_cast<int*>(sScale + 2 * kKeyTile);   // [2][kKeyTile]
-  __shared__ int sTmp[kScoreThreads / 32], sFound[3];
+  uint2* sQ = reinterpret_cast<uint2*>(smem);  // [group, tile][k-step][lane]
+  float* sGain = reinterpret_cast<float*>(smem + size_t(groups) * NT * C::kSteps * 256);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g8 = lane >> 2, u = lane & 3;
 
-  // ---- which rows -----------------------------------------------------------------------
-  const int tile = blockIdx.x / p.chunks, kc = blockIdx.x % p.chunks;
-  if (tid == 0) {
-    sFound[0] = -1;
-    if (p.cu == nullptr && p.c0 + tile < p.c1) sFound[0] = sFound[1] = p.c0 + tile, sFound[2] = 1;
-  }
-  __syncthreads();
-  if (p.cu != nullptr) {
-    int base = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kScoreThreads) {
-      int2 r = make_int2(0, 0);
-      if (b0 + tid < p.B) r = rows_of(p, b0 + tid, false);
-      r.x = max(r.x, p.c0);
-      r.y = min(r.y, p.c1);
-      const int mine = r.y > r.x ? (r.y - r.x + C::kRows - 1) / C::kRows : 0;
-      int total;
-      const int before = base + block_scan<kScoreThreads>(mine, sTmp, total) - mine;
-      if (tile >= before && tile < before + mine) {
-        const int t0 = r.x + (tile - before) * C::kRows;
-        sFound[0] = b0 + tid, sFound[1] = t0, sFound[2] = min(C::kRows, r.y - t0);
-      }
-      base += total;
-      __syncthreads();
-      if (tile < base) break;
-    }
-  }
-  const int b = sFound[0];
-  if (b < 0) return;
-  const int t0 = sFound[1], n = sFound[2];
-  // row t sees len - (last - t) tokens
-  const int last = rows_of(p, b, false).y - 1, len = length_of(p, b, false);
-  const int f_most = max(len - (last - (t0 + n - 1)), 0) / p.block;
-  if (f_most <= p.top) return;  // every row of the tile takes all its blocks
-  const int k0 = kc * p.chunk_tiles * kKeyTile, k1 = min(k0 + p.chunk_tiles * kKeyTile, f_most);
-  if (k0 >= k1) return;
-
-  const uint32_t key_s = smem_addr(smem), q_s = smem_addr(sQ);
-  // 16-byte chunk c of row r lies at chunk c ^ (r mod 8) of the row (64-byte rows:
-  // c ^ (r / 2 mod 4)), so the 8 rows of a matrix fall into different banks.
-  auto swz = [](int r, int c) { return DI == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3); };
-  auto load_tile = [&](int kt, int buf) {
-    const int r = tid >> 1, j = k0 + kt * kKeyTile + r;
-    bool ok = false;
-    int64_t phys = 0;
-    if (j < k1) {
-      const int m = j / p.per_page;
-      const int page = __ldg(p.table + b * p.table_st + m);
-      ok = page >= 0 && page < p.pages;
-      if (!ok && p.err_word != nullptr) atomicOr(p.err_word, QSA_ERRBIT_SLOT_RANGE);
-      phys = ok ? int64_t(page) * p.per_page + (j - m * p.per_page) : 0;
-    }
-    const int8_t* src = p.codes + phys * p.code_st;
-#pragma unroll
-    for (int i = 0; i < DI / 32; ++i) {
-      const int c = (tid & 1) * (DI / 32) + i;
-      cp_async_16(key_s + buf * C::kTileBytes + r * DI + (swz(r, c) << 4), ok ? src + c * 16 : p.codes, ok);
-    }
-    if ((tid & 1) == 0) {
-      sScale[buf * kKeyTile + r] = ok ? __ldg(p.scales + phys) : 0.f;
-      sValid[buf * kKeyTile + r] = ok;
-    }
+  // units of sequence b's rows in this chunk: as many as if every tile saw all of its blocks
+  auto rows_here = [&](int b) {
+    int2 r = rows_of(p, b, false);
+    r.x = max(r.x, p.c0);
+    r.y = min(r.y, p.c1);
+    return r;
   };
-  load_tile(0, 0);
-  cp_async_commit();
-
-  // ---- the rows' codes and gains ----------------------------------------------------------
-  {
-    constexpr int kLanes = DI / 8, kVec = 32 / kLanes;  // lanes of a vector, vectors of a warp
-    const int l = lane % kLanes;
-    for (int v0 = warp * kVec; v0 < groups * C::kCols; v0 += (kScoreThreads / 32) * kVec) {
-      const int v = v0 + lane / kLanes;  // (kCols is a multiple of kVec)
-      const int g = v / C::kCols, c = v % C::kCols;
-      const int x = (c >> 3) * 2 + (c & 1);
-      const int row = ((c & 7) >> 1) * C::kRx + x / HP, head = g * 16 + x % HP;
-      const bool live = row < n && head < p.Hi;
-      uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-      if (live)
-        raw = *reinterpret_cast<const uint4*>(p.q + (t0 + row) * p.q_st + head * p.q_sh + l * 8);
-      float xs[8];
-      bf16x8_to_f32(raw, xs);
-      uint32_t top = top_bits(xs);
+  auto units_at = [&](int b) -> int64_t {
+    if (b >= p.B) return 0;
+    const int2 r = rows_here(b);
+    const int f = length_of(p, b, false) / p.block;
+    if (r.y <= r.x || f <= p.top) return 0;
+    return int64_t((r.y - r.x + C::kRows - 1) / C::kRows) * ((f + kKeyTile - 1) / kKeyTile);
+  };
+  int64_t total = 0;
+  for (int b = lane; b < p.B; b += 32) total += units_at(b);
 #pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float scale = code_scale(__uint_as_float(top));
-      *reinterpret_cast<uint2*>(sQ + v * DI + (swz(c, l >> 1) << 4) + (l & 1) * 8) = int8x8_codes(xs, scale);
-      if (l == 0) sGain[v] = live ? __fmul_rn(p.weight[(t0 + row) * p.w_st + head], scale) : 0.f;
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  const int64_t u0 = total * blockIdx.x / gridDim.x, u1 = total * (blockIdx.x + 1) / gridDim.x;
+  if (u0 == u1) return;
+  int b = 0;
+  int64_t before = 0;  // units of the sequences before b
+  for (;; b += 32) {   // (every warp for itself)
+    const int64_t n = units_at(b + lane);
+    int64_t to = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, to, o);
+      if (lane >= o) to += y;
     }
+    const uint32_t past = __ballot_sync(0xffffffffu, before + to > u0);
+    if (past != 0u) {
+      const int l = __ffs(past) - 1;
+      before += __shfl_sync(0xffffffffu, to - n, l);
+      b += l;
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, to, 31);
   }
 
-  const int tiles = (k1 - k0 + kKeyTile - 1) / kKeyTile;
-  const int u = lane & 3;
-  for (int kt = 0; kt < tiles; ++kt) {
-    const int buf = kt & 1;
-    cp_async_wait<0>();
-    __syncthreads();  // the tile has landed, and nothing reads the other buffer any more
-    if (kt + 1 < tiles) {
-      load_tile(kt + 1, buf ^ 1);
-      cp_async_commit();
+  for (int64_t at = u0; at < u1;) {
+    // ---- a piece: key tiles of one tile of rows ------------------------------------------------
+    const int2 r = rows_here(b);
+    const int last = rows_of(p, b, false).y - 1, len = length_of(p, b, false);
+    const int per_tile = (len / p.block + kKeyTile - 1) / kKeyTile;
+    const int tile = int((at - before) / per_tile), kt = int(at - before - int64_t(tile) * per_tile);
+    const int64_t end = min(u1, before + int64_t(tile + 1) * per_tile);
+    const int t0 = r.x + tile * C::kRows, n = min(C::kRows, r.y - t0);
+    const int f_most = max(len - (last - (t0 + n - 1)), 0) / p.block;
+    const int k0 = kt * kKeyTile, k1 = min(k0 + int(end - at) * kKeyTile, f_most);
+    const int subs = f_most <= p.top ? 0 : (k1 - k0 + 15) / 16;  // (0: every row takes all its blocks)
+    const int32_t* table = p.table + b * p.table_st;
+
+    // pages of blocks k0 + 16 s + g8 and + 8; then their codes
+    int page[2], off[2];
+    auto lookup = [&](int sub) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int j = k0 + sub * 16 + g8 + 8 * h;
+        page[h] = -1;
+        off[h] = -1;  // no such block
+        if (j < k1) {
+          int m = j;
+          if (p.per_page > 1) {
+            m = __umulhi(uint32_t(j), p.page_magic);
+            if (int64_t(m) * p.per_page > j) --m;
+          }
+          off[h] = j - m * p.per_page;
+          page[h] = __ldg(table + m);
+        }
+      }
+    };
+    uint4 key[2][DI / 64], next_key[2][DI / 64];
+    float scale[2], next_scale[2];
+    auto fetch = [&]() {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool ok = page[h] >= 0 && page[h] < p.pages;
+        if (!ok && off[h] >= 0 && p.err_word != nullptr) atomicOr(p.err_word, QSA_ERRBIT_SLOT_RANGE);
+        const int64_t phys = ok ? int64_t(page[h]) * p.per_page + off[h] : 0;
+        next_scale[h] = __int_as_float(0x7fffffff);
+#pragma unroll
+        for (int i = 0; i < DI / 64; ++i) next_key[h][i] = make_uint4(0u, 0u, 0u, 0u);
+        if (ok) {
+          next_scale[h] = __ldg(p.scales + phys);
+#pragma unroll
+          for (int i = 0; i < DI / 64; ++i)
+            next_key[h][i] = __ldg(reinterpret_cast<const uint4*>(p.codes + phys * p.code_st + i * 64 + u * 16));
+        }
+      }
+    };
+    if (warp < subs) {
+      lookup(warp);
+      fetch();
+      lookup(warp + kScoreThreads / 32);
     }
-    uint32_t a[DI / 32][4];
+
+    // ---- the rows' codes and gains ----------------------------------------------------------
+    __syncthreads();  // (the last piece's)
+    for (int x = warp; subs > 0 && x < groups * NT; x += kScoreThreads / 32) {
+      const int i = x % NT, c = 2 * i + (g8 & 1), row = (g8 >> 1) * C::kRx + c / HP, head = x / NT * 16 + c % HP;
+      const bool live = row < n && head < p.Hi;
+      uint4 raw[DI / 64][2];
 #pragma unroll
-    for (int ks = 0; ks < DI / 32; ++ks) {
-      const int r = warp * 16 + (lane & 15);
-      ldmatrix_x4(a[ks], key_s + buf * C::kTileBytes + r * DI + (swz(r, ks * 2 + (lane >> 4)) << 4));
+      for (int k = 0; k < DI / 64; ++k) raw[k][0] = raw[k][1] = make_uint4(0u, 0u, 0u, 0u);
+      float gain = 0.f;
+      if (live) {
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (t0 + row) * p.q_st + head * p.q_sh + u * 16);
+#pragma unroll
+        for (int k = 0; k < DI / 64; ++k) raw[k][0] = src[k * 8], raw[k][1] = src[k * 8 + 1];
+        gain = p.weight[(t0 + row) * p.w_st + head];
+      }
+      float xs[DI / 64][2][8];
+      uint32_t top = 0u;
+#pragma unroll
+      for (int k = 0; k < DI / 64; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          bf16x8_to_f32(raw[k][e], xs[k][e]);
+          top = max(top, top_bits(xs[k][e]));
+        }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const float s = code_scale(__uint_as_float(top));
+#pragma unroll
+      for (int k = 0; k < DI / 64; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) sQ[(x * C::kSteps + 2 * k + e) * 32 + lane] = int8x8_codes(xs[k][e], s);
+      if (u == 0) sGain[x * 8 + g8] = live ? __fmul_rn(gain, s) : 0.f;
     }
-    float sum[C::kRx][2];  // [row of the thread][key lane / 4, key lane / 4 + 8]
-    for (int g = 0; g < groups; ++g) {
-      int acc[NT][4];
+    __syncthreads();
+    // in registers where there is room
+    constexpr bool kHold = NT <= 2;
+    uint2 q[kHold ? NT : 1][C::kSteps];
+    float gain[kHold ? C::kPer : 1];
+    if constexpr (kHold) {
 #pragma unroll
-      for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0;
+      for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int ks = 0; ks < DI / 32; ++ks) {
+        for (int ks = 0; ks < C::kSteps; ++ks) q[i][ks] = sQ[(i * C::kSteps + ks) * 32 + lane];
 #pragma unroll
-        for (int i = 0; i < NT; i += 2) {
-          // four matrices: both 16-byte halves of tile i, then of tile i + 1 (NT = 1: tile 0 again)
-          const int c = (NT > 1 ? i + (lane >> 4) : i) * 8 + (lane & 7);
-          uint32_t bq[4];
-          ldmatrix_x4(bq, q_s + (g * C::kCols + c) * DI + (swz(c, ks * 2 + ((lane >> 3) & 1)) << 4));
-          mma_s8_16832(acc[i], a[ks], bq[0], bq[1]);
-          if constexpr (NT > 1) mma_s8_16832(acc[i + 1], a[ks], bq[2], bq[3]);
+      for (int x = 0; x < C::kPer; ++x) gain[x] = sGain[(x >> 1) * 8 + 2 * u + (x & 1)];
+    }
+
+    for (int sub = warp; sub < subs; sub += kScoreThreads / 32) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        scale[h] = next_scale[h];
+#pragma unroll
+        for (int i = 0; i < DI / 64; ++i) key[h][i] = next_key[h][i];
+      }
+      fetch();
+      lookup(sub + 2 * (kScoreThreads / 32));
+      float sum[C::kRx][2];  // [row of the thread][block g8, block g8 + 8]
+      for (int g = 0; g < groups; ++g) {
+        int acc[NT][4];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0;
+#pragma unroll
+        for (int ks = 0; ks < C::kSteps; ++ks) {
+          const uint4 k0w = key[0][ks >> 1], k1w = key[1][ks >> 1];
+          const uint32_t a[4] = {ks & 1 ? k0w.z : k0w.x, ks & 1 ? k1w.z : k1w.x, ks & 1 ? k0w.w : k0w.y,
+                                 ks & 1 ? k1w.w : k1w.y};
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            uint2 c;
+            if constexpr (kHold) c = q[i][ks]; else c = sQ[((g * NT + i) * C::kSteps + ks) * 32 + lane];
+            mma_s8_16832(acc[i], a, c.x, c.y);
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < C::kPer; ++x) {
+          float gx;
+          if constexpr (kHold) gx = gain[x]; else gx = sGain[(g * NT + (x >> 1)) * 8 + 2 * u + (x & 1)];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // (a dot of 128 codes is below 2^24: exact)
+            const float term = __fmul_rn(gx, float(max(acc[x >> 1][h * 2 + (x & 1)], 0)));
+            float& s = sum[x / HP][h];
+            s = (x % HP == 0 && g == 0) ? term : __fadd_rn(s, term);
+          }
         }
       }
 #pragma unroll
-      for (int x = 0; x < C::kPer; ++x) {
-        const float gain = sGain[g * C::kCols + (x >> 1) * 8 + 2 * u + (x & 1)];
+      for (int h = 0; h < 2; ++h) {
+        const int j = k0 + sub * 16 + g8 + 8 * h;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          // (a dot of 128 codes is below 2^24: exact)
-          const float term = __fmul_rn(gain, float(max(acc[x >> 1][h * 2 + (x & 1)], 0)));
-          float& s = sum[x / HP][h];
-          s = (x % HP == 0 && g == 0) ? term : __fadd_rn(s, term);
+        for (int i = 0; i < C::kRx; ++i) {
+          const int t = t0 + u * C::kRx + i;
+          if (j < k1 && t < t0 + n)
+            p.scores[(t - p.c0) * p.ld + j] = kept_score(sum[i][h], scale[h]);
         }
       }
     }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = warp * 16 + (lane >> 2) + 8 * h, j = k0 + kt * kKeyTile + r;
-      const float scale = sScale[buf * kKeyTile + r];
-      const bool ok = sValid[buf * kKeyTile + r] != 0;
-#pragma unroll
-      for (int i = 0; i < C::kRx; ++i) {
-        const int t = t0 + u * C::kRx + i;
-        if (t < t0 + n && j < (len - (last - t)) / p.block)
-          p.keys[(t - p.c0) * p.ld + j] = ok ? order_key(__fmul_rn(sum[i][h], scale)) : 0u;
-      }
+    at = end;
+    if (at < u1 && at == before + int64_t((r.y - r.x + C::kRows - 1) / C::kRows) * per_tile) {  // the next sequence
+      before = at;
+      do ++b; while (units_at(b) == 0);
     }
   }
 }
@@ -277,6 +343,7 @@ constexpr int kWideCols = 256;
 constexpr int kWideStages = 6;                     // key tiles in shared memory
 constexpr int kWideQ = 3;                          // Q tiles in shared memory (one more than a producer's lag)
 constexpr int kWideLag = 2;                        // tiles a producer has in flight behind the one it issues
+constexpr int kPrepParts = 4;                      // thread blocks that make a tile's codes
 constexpr int kEpilogueWarps = 16, kProducerWarps = 4;
 constexpr int kWideThreads = 32 * (kEpilogueWarps + kProducerWarps + 1);
 
@@ -321,28 +388,30 @@ __device__ WideTile find_tile(const SelectParams& p, int c0, int c1, int tile, i
 }
 
 // The codes and gains of every tile's rows, laid out as the MMA reads them (no swizzle: 8
-// columns by 16 bytes contiguous), and the list of tiles: blockIdx.x is the tile, blockIdx.y
-// the chunk of rows.
+// columns by 16 bytes contiguous), and the list of tiles: blockIdx.x is the tile and the
+// quarter of its columns, blockIdx.y the chunk of rows.
 template <int DI, int HP>
 __global__ void __launch_bounds__(256) qsa_select_prep_kernel(const SelectParams p, int chunk_rows) {
   constexpr int kLanes = DI / 8, kVec = 32 / kLanes;
   __shared__ int sTmp[8], sFound[4];
   const int c0 = int(min(int64_t(blockIdx.y) * chunk_rows, int64_t(p.Tq)));
   const int c1 = int(min(int64_t(c0) + chunk_rows, int64_t(p.Tq)));
-  const WideTile w = find_tile<256>(p, c0, c1, blockIdx.x, kWideCols / HP, sTmp, sFound);
-  const int64_t slot = int64_t(blockIdx.y) * gridDim.x + blockIdx.x;
-  if (threadIdx.x == 0) p.tiles[slot] = make_int4(w.b, w.t0, w.n, w.b < 0 ? 0 : w.f);
+  const int tile = blockIdx.x / kPrepParts, part = blockIdx.x % kPrepParts;
+  const WideTile w = find_tile<256>(p, c0, c1, tile, kWideCols / HP, sTmp, sFound);
+  const int64_t slot = int64_t(blockIdx.y) * (gridDim.x / kPrepParts) + tile;
+  if (threadIdx.x == 0 && part == 0) p.tiles[slot] = make_int4(w.b, w.t0, w.n, w.b < 0 ? 0 : w.f);
   if (w.b < 0 || w.f == 0) return;
   uint8_t* dst = p.tile_q + slot * wide_tile_bytes(DI);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % kLanes;
-  constexpr int kRounds = kWideCols / (8 * kVec);  // vectors of a thread
+  constexpr int kRounds = kWideCols / kPrepParts / (8 * kVec);  // vectors of a thread
   constexpr int kAhead = kRounds < 4 ? kRounds : 4;
+  static_assert(kRounds % kAhead == 0, "whole rounds");
   for (int i0 = 0; i0 < kRounds; i0 += kAhead) {
     uint4 raw[kAhead];
     float gain[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int v = ((i0 + u) * 8 + warp) * kVec + lane / kLanes;  // column
+      const int v = part * (kWideCols / kPrepParts) + ((i0 + u) * 8 + warp) * kVec + lane / kLanes;  // column
       const int row = v / (2 * HP) * 2 + (v & 1), head = (v % (2 * HP)) >> 1;
       raw[u] = make_uint4(0u, 0u, 0u, 0u);
       gain[u] = 0.f;
@@ -353,7 +422,7 @@ __global__ void __launch_bounds__(256) qsa_select_prep_kernel(const SelectParams
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int v = ((i0 + u) * 8 + warp) * kVec + lane / kLanes;
+      const int v = part * (kWideCols / kPrepParts) + ((i0 + u) * 8 + warp) * kVec + lane / kLanes;
       const int row = v / (2 * HP) * 2 + (v & 1), head = (v % (2 * HP)) >> 1;
       float xs[8];
       bf16x8_to_f32(raw[u], xs);
@@ -396,8 +465,8 @@ template <int DI>
 struct Wide {
   static constexpr int kKeyBytes = kKeyTile * DI;
   static constexpr int kQBytes = wide_tile_bytes(DI);
-  // key stages, Q tiles, the stages' scales and valid marks
-  static constexpr int kSmem = kWideStages * kKeyBytes + kWideQ * kQBytes + kWideStages * kKeyTile * 8;
+  // key stages, Q tiles, the stages' scales
+  static constexpr int kSmem = kWideStages * kKeyBytes + kWideQ * kQBytes + kWideStages * kKeyTile * 4;
 };
 
 // One thread block per SM walks an equal share of all (tile of rows, tile of keys) pairs.
@@ -414,7 +483,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem + kWideStages * C::kKeyBytes;
   float* sScale = reinterpret_cast<float*>(sQ + kWideQ * C::kQBytes);             // [stages][128]
-  int* sValid = reinterpret_cast<int*>(sScale + kWideStages * kKeyTile);     // [stages][128]
   // key stage full / free, Q full / free, accumulator full / free
   __shared__ __align__(8) uint64_t sBar[2 * kWideStages + 2 * kWideQ + 4];
   __shared__ uint32_t sTmem;
@@ -527,10 +595,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
       for (int c = 0; c < DI / 16; ++c)
         cp_async_16(dst + (c >> 1) * (kKeyTile * 32) + (c & 1) * 128, ok ? src + c * 16 : src, ok);
-      sValid[stage * kKeyTile + r] = !bad;
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(smem_addr(sScale + stage * kKeyTile + r)),
-                   "l"(p.scales + phys), "r"(ok ? 4 : 0)
-                   : "memory");
+      if (ok)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(smem_addr(sScale + stage * kKeyTile + r)),
+                     "l"(p.scales + phys)
+                     : "memory");
+      else
+        sScale[stage * kKeyTile + r] = __int_as_float(0x7fffffff);
       cp_async_commit();
       if (i >= kWideLag) {  // the tile issued kWideLag before has landed: hand it over
         cp_async_wait<kWideLag>();
@@ -604,14 +674,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const float scale = sScale[stage * kKeyTile + r];
-      const bool valid = sValid[stage * kKeyTile + r] != 0;
-      const bool any_bad = __any_sync(0xffffffffu, !valid);
       const int j = kt * kKeyTile + r;
       const uint64_t scale2 = pack2(scale, scale);
       const float* gains = reinterpret_cast<const float*>(sQ + (qn % kWideQ) * C::kQBytes + kWideCols * DI) + part * kPartCols;
       const int row0 = part * kPartRows;
-      uint32_t* out = p.keys + int64_t(w.y + row0 - p.c0) * p.ld + j;
-      const bool store = j < p.ld;
+      uint32_t at = uint32_t(w.y + row0 - p.c0) * uint32_t(p.ld) + uint32_t(j);  // (a chunk has fewer than 2^30)
+      const int rows = j < p.ld ? w.z - row0 : 0;  // that this lane stores
       const uint64_t minus = pack2(-8388608.f, -8388608.f), zero = pack2(0.f, 0.f);
       uint64_t sum = zero;
 #pragma unroll
@@ -641,11 +709,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
               unpack2(fma2(sum, scale2, zero), s[0], s[1]);  // (-0 becomes +0)
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                const uint32_t u = __float_as_uint(fmaxf(s[k], -__builtin_huge_valf()));  // NaN: -infinity
-                uint32_t key = u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
-                if (any_bad && !valid) key = 0u;
-                if (store && row0 + 2 * pair + k < w.z) *out = key;
-                out += p.ld;
+                if (2 * pair + k < rows) p.scores[at] = fmaxf(s[k], -__builtin_huge_valf());  // (NaN: -infinity)
+                at += uint32_t(p.ld);
               }
             }
           }
@@ -672,7 +737,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 
 constexpr int kBins = 512;     // of a histogram: 16 per lane of one warp
 constexpr int kSample = 1024;  // keys that estimate the border of a long row
-constexpr int kBatch = 2;      // 16-byte loads of keys per thread and step
 constexpr int kWindow = 1024;  // most words of the marks: 32,768 blocks at a time
 
 // The border of a row: blocks of a larger key are taken, of `equal` equal ones the first `want`.
@@ -681,25 +745,108 @@ struct Border {
   int want, equal;
 };
 
-struct ChooseShared {
+// Blocks to slots through a sequence's pages.
+struct SlotMap {
+  const SelectParams& p;
+  const int32_t* table;
+  __device__ __forceinline__ int first_slot(int j) const {  // of block j, or -1
+    int m = j;
+    if (p.per_page > 1) {
+      m = __umulhi(uint32_t(j), p.page_magic);  // j / per_page, or one more
+      if (int64_t(m) * p.per_page > j) --m;
+    }
+    const int page = __ldg(table + m);
+    if (page < 0 || page >= p.pages) {
+      if (p.err_word != nullptr) atomicOr(p.err_word, QSA_ERRBIT_SLOT_RANGE);
+      return -1;
+    }
+    return page * p.page_size + (j - m * p.per_page) * p.block;
+  }
+};
+
+// A list of blocks becomes a list of their first slots, four page lookups of a thread at once.
+template <int THREADS>
+__device__ __forceinline__ void list_slots(const SlotMap& map, int* list, int n, int tid) {
+  const SelectParams& p = map.p;
+  bool bad = false;
+  for (int i0 = tid; i0 < n; i0 += 4 * THREADS) {
+    int off[4], page[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * THREADS;
+      page[u] = 0;
+      off[u] = 0;
+      if (i >= n) continue;
+      const int j = list[i];
+      int m = j;
+      if (p.per_page > 1) {
+        m = __umulhi(uint32_t(j), p.page_magic);  // j / per_page, or one more
+        if (int64_t(m) * p.per_page > j) --m;
+      }
+      off[u] = (j - m * p.per_page) * p.block;
+      page[u] = __ldg(map.table + m);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const bool ok = page[u] >= 0 && page[u] < p.pages;
+      bad |= !ok;
+      if (i0 + u * THREADS < n) list[i0 + u * THREADS] = ok ? page[u] * p.page_size + off[u] : -1;
+    }
+  }
+  if (bad && p.err_word != nullptr) atomicOr(p.err_word, QSA_ERRBIT_SLOT_RANGE);
+}
+
+// Row t's output from the first slots of its taken blocks, by THREADS threads.
+template <int THREADS>
+__device__ __forceinline__ void write_row(const SelectParams& p, const SlotMap& map, int t, int tid, const int* sList,
+                                          int f, int taken, int seen) {
+  int32_t* out = p.out + t * p.out_st;
+  const int W = p.top * p.block + p.block - 1, full = taken * p.block, tail = seen - f * p.block;
+  if (p.block == 4) {  // (the usual micro-block: no division)
+#pragma unroll 8
+    for (int w = tid; w < full; w += THREADS) {
+      const int s = sList[w >> 2];
+      out[w] = s < 0 ? -1 : s + (w & 3);
+    }
+  } else {
+    for (int w = tid; w < full; w += THREADS) {
+      const int i = p.block == 1 ? w : int(__umulhi(uint32_t(w), p.block_magic));  // w / block (w below 2^14)
+      out[w] = sList[i] < 0 ? -1 : sList[i] + (w - i * p.block);
+    }
+  }
+  const int tail_slot = tail > 0 ? map.first_slot(f) : -1;
+  for (int w = full + tid; w < W; w += THREADS)
+    out[w] = w < full + tail && tail_slot >= 0 ? tail_slot + (w - full) : -1;
+  if (tid == 0) p.width[t] = full + tail;
+}
+
+struct alignas(16) ChooseShared {  // (the histogram is read 16 bytes at a time)
   int hist[kBins];
   uint32_t few[32];
   uint32_t lo, hi;
   int n_few, bin, above, count, n;
 };
 
-// mask |= bit when key >= low: two instructions.
-__device__ __forceinline__ void keep_bit(uint32_t& mask, uint32_t key, uint32_t low, uint32_t bit) {
-  asm("{\n  .reg .pred q;\n  setp.ge.u32 q, %1, %2;\n  @q or.b32 %0, %0, %3;\n}\n" : "+r"(mask) : "r"(key), "r"(low), "r"(bit));
+constexpr int kPickWarps = 4;    // rows of a thread block of the kernel for short rows
+constexpr int kPickKeys = 2048;  // most blocks of such a row
+
+// mask |= bit when x >= low: two instructions.
+__device__ __forceinline__ void keep_bit(uint32_t& mask, float x, float low, uint32_t bit) {
+  asm("{\n  .reg .pred q;\n  setp.ge.f32 q, %1, %2;\n  @q or.b32 %0, %0, %3;\n}\n" : "+r"(mask) : "f"(x), "f"(low), "r"(bit));
 }
 
 // The want-th largest (1 <= want <= n) of the keys key_at(0 .. n - 1), by histograms of the
 // key range that still holds it; the last step ranks at most 32 keys within each warp.
 // Without EXACT: a key at most that one with few keys between them (`key` alone is meant).
+template <int THREADS>
+__device__ __forceinline__ void sync_all() {
+  if constexpr (THREADS == 32) __syncwarp(); else __syncthreads();
+}
+
 template <int THREADS, bool EXACT, class F>
 __device__ Border kth_largest(int n, int want, F key_at, ChooseShared& sh) {
-  const int tid = threadIdx.x, lane = tid & 31;
-  __syncthreads();  // (sh and the keys)
+  const int tid = THREADS == 32 ? threadIdx.x & 31 : threadIdx.x, lane = tid & 31;
+  sync_all<THREADS>();  // (sh and the keys)
   if (tid == 0) sh.lo = 0xffffffffu, sh.hi = 0u, sh.n_few = 0;
   for (int i = tid; i < kBins; i += THREADS) sh.hist[i] = 0;
   uint32_t lo = 0xffffffffu, hi = 0u;
@@ -711,12 +858,12 @@ __device__ Border kth_largest(int n, int want, F key_at, ChooseShared& sh) {
   }
   lo = __reduce_min_sync(0xffffffffu, lo);
   hi = __reduce_max_sync(0xffffffffu, hi);
-  __syncthreads();
+  sync_all<THREADS>();
   if (lane == 0 && lo <= hi) {
     atomicMin(&sh.lo, lo);
     atomicMax(&sh.hi, hi);
   }
-  __syncthreads();
+  sync_all<THREADS>();
   const uint32_t least = sh.lo;
   hi = sh.hi;
   // The keys are floats in order: most of a row's lie in a few octaves below the largest, so
@@ -730,7 +877,7 @@ __device__ Border kth_largest(int n, int want, F key_at, ChooseShared& sh) {
       const uint32_t k = key_at(i) - lo;
       if (k <= range) atomicAdd(&sh.hist[k >> shift], 1);
     }
-    __syncthreads();
+    sync_all<THREADS>();
     if (tid < 32) {  // lane i holds bins 511 - 16 i down to 496 - 16 i
       const int first = kBins - 16 * (lane + 1);
       int c[16], mine = 0;
@@ -756,11 +903,11 @@ __device__ Border kth_largest(int n, int want, F key_at, ChooseShared& sh) {
         }
       }
     }
-    __syncthreads();
+    sync_all<THREADS>();
     if (sh.bin < 0) {  // fewer keys than wanted above lo
       lo = least;
       for (int i = tid; i < kBins; i += THREADS) sh.hist[i] = 0;
-      __syncthreads();
+      sync_all<THREADS>();
       continue;
     }
     want -= sh.above;
@@ -775,7 +922,7 @@ __device__ Border kth_largest(int n, int want, F key_at, ChooseShared& sh) {
         const uint32_t k = key_at(i);
         if (k - lo <= hi - lo) sh.few[atomicAdd(&sh.n_few, 1)] = k;
       }
-      __syncthreads();
+      sync_all<THREADS>();
       const uint32_t mine = sh.few[lane < count ? lane : 0];
       int more = 0, same = 0;
       for (int i = 0; i < count; ++i) {
@@ -789,8 +936,109 @@ __device__ Border kth_largest(int n, int want, F key_at, ChooseShared& sh) {
               __shfl_sync(0xffffffffu, same, src)};
     }
     for (int i = tid; i < kBins; i += THREADS) sh.hist[i] = 0;
-    __syncthreads();
+    sync_all<THREADS>();
   }
+}
+
+// Rows of at most kPickKeys blocks, a warp each: its keys lie in the warp's shared memory,
+// nothing is shared between warps, and no barrier is waited for.  Bound: instructions, about
+// two per key and pivot, ten per key to collect the taken ones in order, and the output.
+__global__ void __launch_bounds__(32 * kPickWarps) qsa_select_pick_kernel(const SelectParams p) {
+  extern __shared__ __align__(16) uint32_t dyn[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row_at = blockIdx.x * kPickWarps + warp, t = p.c0 + row_at;
+  if (t >= p.c1) return;
+  __shared__ __align__(16) ChooseShared sSearch[kPickWarps];
+  uint32_t* sKey = dyn + warp * (p.cap + (p.top + 3) / 4 * 4);
+  int* sList = reinterpret_cast<int*>(sKey + p.cap);
+  int b = -1;
+  if (p.cu == nullptr) {
+    if (t < p.B) b = t;
+  } else {
+    for (int i0 = 0; i0 < p.B; i0 += 32) {
+      bool mine = false;
+      if (i0 + lane < p.B) {
+        const int2 r = rows_of(p, i0 + lane, row_at == 0 && p.c0 == 0);
+        mine = t >= r.x && t < r.y;
+      }
+      const uint32_t m = __ballot_sync(0xffffffffu, mine);
+      if (m != 0u) b = i0 + 31 - __clz(m);  // (offsets that overlap: the last one)
+    }
+  }
+  if (b < 0) return;
+  const int last = rows_of(p, b, false).y - 1, len = length_of(p, b, lane == 0);
+  const int seen = max(len - (last - t), 0), f = seen / p.block, taken = min(f, p.top);
+  const SlotMap map{p, p.table + b * p.table_st};
+  if (f <= p.top) {
+    for (int j = lane; j < f; j += 32) sList[j] = map.first_slot(j);
+  } else {
+    // blocks that are taken whatever they score do not take part in the search: key 0
+    const uint4* row4 = reinterpret_cast<const uint4*>(p.scores + int64_t(row_at) * p.ld) + lane;
+    uint4* key4 = reinterpret_cast<uint4*>(sKey) + lane;
+    auto forced = [&](int j) { return j < p.sink || j >= f - p.local; };
+#pragma unroll 4
+    for (int i = 0; i * 128 < f; ++i) {
+      const int j = i * 128 + lane * 4;
+      uint4 k = make_uint4(0u, 0u, 0u, 0u);
+      if (j < f) k = __ldg(row4 + i * 32);
+      k = make_uint4(order_key(k.x), order_key(k.y), order_key(k.z), order_key(k.w));
+      if (i * 128 < p.sink || i * 128 + 128 > f - p.local) {
+        if (forced(j)) k.x = 0u;  // (or past the end)
+        if (forced(j + 1)) k.y = 0u;
+        if (forced(j + 2)) k.z = 0u;
+        if (forced(j + 3)) k.w = 0u;
+      }
+      key4[i * 32] = k;
+    }
+    __syncwarp();
+    const int want = p.top - p.sink - p.local;
+    Border border{0xffffffffu, 0, 0};
+    if (want > 0) border = kth_largest<32, true>(f, want, [&](int i) { return sKey[i]; }, sSearch[warp]);
+    const bool all_same = border.want == border.equal;
+    const uint32_t below = (1u << lane) - 1u, least = all_same ? border.key : border.key + 1u;
+    int have = 0, same = 0;
+    for (int i = 0; i * 128 < f; ++i) {  // a lane has four neighbours
+      const uint4 k4 = key4[i * 32];
+      const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+      const int j = i * 128 + lane * 4;
+      const bool edge = i * 128 < p.sink || i * 128 + 128 > f - p.local;
+      uint32_t take[4];
+      int at = have, mine = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        bool in = k[e] >= least;
+        if (edge || least == 0u) in = j + e < f && ((want > 0 && in && !forced(j + e)) || forced(j + e));
+        take[e] = __ballot_sync(0xffffffffu, in);
+      }
+      if (!all_same) {  // of equal keys the first ones
+        uint32_t eq[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          eq[e] = __ballot_sync(0xffffffffu, j + e < f && k[e] == border.key && !forced(j + e));
+        int before = same;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) before += __popc(eq[e] & below);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool is_eq = (eq[e] >> lane) & 1;
+          take[e] |= __ballot_sync(0xffffffffu, is_eq && before < border.want);
+          before += is_eq;
+          same += __popc(eq[e]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) at += __popc(take[e] & below);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if ((take[e] >> lane) & 1) sList[at + mine++] = j + e;
+        have += __popc(take[e]);
+      }
+    }
+    __syncwarp();
+    list_slots<32>(map, sList, p.top, lane);
+  }
+  __syncwarp();
+  write_row<32>(p, map, t, lane, sList, f, taken, seen);
 }
 
 // One thread block per row.  A row of at most `cap` blocks has its keys in shared memory.  Of
@@ -803,7 +1051,8 @@ __device__ Border kth_largest(int n, int want, F key_at, ChooseShared& sh) {
 // (radix passes over the whole row, four reads and a conflicting shared-memory atomic per key
 // and pass, took 165 us per 1,024 rows of 15,500 blocks).
 template <int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : 1) qsa_select_choose_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : THREADS == 256 ? 4 : 1) qsa_select_choose_kernel(const SelectParams p) {
+  constexpr int kBatch = THREADS == 1024 ? 4 : 2;  // 16-byte loads of keys per thread and step
   extern __shared__ __align__(16) uint32_t dyn[];
   uint32_t* sKey = dyn;                                       // [cap]
   int* sIdx = reinterpret_cast<int*>(sKey + p.cap);           // [cap], absent when every row fits
@@ -828,29 +1077,16 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : 1) qsa_select_c
   const int last = rows_of(p, b, false).y - 1, len = length_of(p, b, tid == 0);
   const int seen = max(len - (last - t), 0);
   const int f = seen / p.block, taken = min(f, p.top);
-  const uint32_t* row = p.keys + blockIdx.x * p.ld;
-  const int32_t* table = p.table + b * p.table_st;
-  auto first_slot = [&](int j) {  // of block j, or -1
-    int m = j;
-    if (p.per_page > 1) {
-      m = __umulhi(uint32_t(j), p.page_magic);  // j / per_page, or one more
-      if (int64_t(m) * p.per_page > j) --m;
-    }
-    const int page = __ldg(table + m);
-    if (page < 0 || page >= p.pages) {
-      if (p.err_word != nullptr) atomicOr(p.err_word, QSA_ERRBIT_SLOT_RANGE);
-      return -1;
-    }
-    return page * p.page_size + (j - m * p.per_page) * p.block;
-  };
+  const float* row = p.scores + blockIdx.x * p.ld;
+  const SlotMap map{p, p.table + b * p.table_st};
   if (f <= p.top) {
-    for (int j = tid; j < f; j += THREADS) sList[j] = first_slot(j);
+    for (int j = tid; j < f; j += THREADS) sList[j] = map.first_slot(j);
   } else {
     // blocks that are taken whatever they score do not take part in the search
     const int want = p.top - p.sink - p.local;
     auto forced = [&](int j) { return j < p.sink || j >= f - p.local; };
-    auto searched = [&](int j, uint32_t k) { return forced(j) ? 0u : k; };
-    auto in_row = [&](int j) { return searched(j, __ldg(row + j)); };
+    auto searched = [&](int j, uint32_t score) { return forced(j) ? 0u : order_key(score); };
+    auto in_row = [&](int j) { return searched(j, __float_as_uint(__ldg(row + j))); };
     const uint4* row4 = reinterpret_cast<const uint4*>(row);  // (ld is a multiple of 32)
     auto in_list = [&](int i) { return sKey[i]; };
     Border border{0xffffffffu, 0, 0};
@@ -894,6 +1130,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : 1) qsa_select_c
         __syncthreads();
         if (tid == 0) sh.n = 0;
         __syncthreads();
+        const float least = key_score(low);
         uint4 raw[kBatch], next[kBatch];
         auto load = [&](int i0) {
 #pragma unroll
@@ -907,18 +1144,20 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : 1) qsa_select_c
 #pragma unroll
           for (int u = 0; u < kBatch; ++u) raw[u] = next[u];
           load(i0 + THREADS * kBatch);
-          uint32_t k[4 * kBatch], keep = 0u;  // a bit per key of this lane
+          float k[4 * kBatch];
+          uint32_t keep = 0u;  // a bit per score of this lane
 #pragma unroll
           for (int u = 0; u < kBatch; ++u)
-            k[4 * u] = raw[u].x, k[4 * u + 1] = raw[u].y, k[4 * u + 2] = raw[u].z, k[4 * u + 3] = raw[u].w;
+            k[4 * u] = __uint_as_float(raw[u].x), k[4 * u + 1] = __uint_as_float(raw[u].y),
+            k[4 * u + 2] = __uint_as_float(raw[u].z), k[4 * u + 3] = __uint_as_float(raw[u].w);
           if (i0 * 4 >= p.sink && (i0 + 32 + (kBatch - 1) * THREADS) * 4 <= f - p.local) {
 #pragma unroll
-            for (int x = 0; x < 4 * kBatch; ++x) keep_bit(keep, k[x], low, 1u << x);
+            for (int x = 0; x < 4 * kBatch; ++x) keep_bit(keep, k[x], least, 1u << x);
           } else {
 #pragma unroll
             for (int x = 0; x < 4 * kBatch; ++x) {
               const int j = (i0 + lane + (x >> 2) * THREADS) * 4 + (x & 3);
-              keep |= j < f && !forced(j) && k[x] >= low ? 1u << x : 0u;
+              keep |= j < f && !forced(j) && k[x] >= least ? 1u << x : 0u;
             }
           }
           const int mine = __popc(keep);
@@ -942,7 +1181,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : 1) qsa_select_c
         const int n = sh.n, room = min(n, p.cap);
         if (n < want) break;
 #pragma unroll 4
-        for (int i = tid; i < room; i += THREADS) sKey[i] = __ldg(row + sIdx[i]);
+        for (int i = tid; i < room; i += THREADS) sKey[i] = order_key(__float_as_uint(__ldg(row + sIdx[i])));
         border = kth_largest<THREADS, true>(room, want, in_list, sh);
         if (n == room) listed = n;
         if (n == room || border.key == low) break;
@@ -1004,27 +1243,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : 1) qsa_select_c
       same += total_same;
     }
     __syncthreads();
-    for (int i = tid; i < p.top; i += THREADS) sList[i] = first_slot(sList[i]);
+    list_slots<THREADS>(map, sList, p.top, tid);
   }
   __syncthreads();
-  int32_t* out = p.out + t * p.out_st;
-  const int W = p.top * p.block + p.block - 1, full = taken * p.block, tail = seen - f * p.block;
-  if (p.block == 4) {  // (the usual micro-block: no division)
-#pragma unroll 4
-    for (int w = tid; w < full; w += THREADS) {
-      const int s = sList[w >> 2];
-      out[w] = s < 0 ? -1 : s + (w & 3);
-    }
-  } else {
-    for (int w = tid; w < full; w += THREADS) {
-      const int i = p.block == 1 ? w : int(__umulhi(uint32_t(w), p.block_magic));  // w / block (w below 2^14)
-      out[w] = sList[i] < 0 ? -1 : sList[i] + (w - i * p.block);
-    }
-  }
-  const int tail_slot = tail > 0 ? first_slot(f) : -1;
-  for (int w = full + tid; w < W; w += THREADS)
-    out[w] = w < full + tail && tail_slot >= 0 ? tail_slot + (w - full) : -1;
-  if (tid == 0) p.width[t] = full + tail;
+  write_row<THREADS>(p, map, t, tid, sList, f, taken, seen);
 }
 
 // ---- the launch --------------------------------------------------------------------------
@@ -1038,6 +1260,7 @@ int64_t blocks_ld(int32_t P, int32_t page_size, int32_t block) {
 int32_t chunk_rows(int32_t Tq, int64_t ld) {
   int64_t n = ld > 0 ? kChunkBytes / (ld * 4) : Tq;
   n = n < kMinChunkRows ? kMinChunkRows : n;
+  if (ld > 0 && n * ld >= (1 << 30)) n = ((1 << 30) - 1) / ld;
   return int32_t(n < Tq ? n : Tq);
 }
 
@@ -1048,17 +1271,11 @@ cudaError_t launch_score(SelectParams& p, int groups, int num_sms, cudaStream_t 
   cudaError_t e = cudaFuncSetAttribute(qsa_select_score_kernel<DI, HP, NT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
+  // as many blocks as the device holds, or as there are units at most
   const int rows = p.c1 - p.c0;
-  // a sequence adds at most one partial tile
   const int64_t row_tiles = p.cu == nullptr ? rows : rows / C::kRows + (p.B < rows ? p.B : rows);
-  const int64_t key_tiles = (p.ld + kKeyTile - 1) / kKeyTile;
-  // up to 8 key tiles to a thread block, fewer while the blocks do not fill the device twice
-  int64_t per = row_tiles * key_tiles / (4 * int64_t(num_sms));
-  per = per < 1 ? 1 : per > 8 ? 8 : per;
-  p.chunk_tiles = int32_t(per);
-  p.chunks = int32_t((key_tiles + per - 1) / per);
-  if (row_tiles * p.chunks > INT32_MAX) return cudaErrorInvalidConfiguration;
-  qsa_select_score_kernel<DI, HP, NT><<<unsigned(row_tiles * p.chunks), kScoreThreads, smem, st>>>(p, groups);
+  const int64_t most = row_tiles * ((p.ld + kKeyTile - 1) / kKeyTile), all = int64_t(num_sms) * kScoreBlocks;
+  qsa_select_score_kernel<DI, HP, NT><<<unsigned(most < all ? most : all), kScoreThreads, smem, st>>>(p, groups);
   return cudaGetLastError();
 }
 
@@ -1080,7 +1297,7 @@ int64_t wide_max_tiles(int32_t rows, int32_t B, int32_t Hi) {  // a sequence add
 
 template <int DI, int HP>
 cudaError_t launch_prep(const SelectParams& p, int chunk_rows, int chunks, cudaStream_t st) {
-  const dim3 grid(unsigned(wide_max_tiles(chunk_rows, p.B, p.Hi)), unsigned(chunks));
+  const dim3 grid(unsigned(wide_max_tiles(chunk_rows, p.B, p.Hi) * kPrepParts), unsigned(chunks));
   qsa_select_prep_kernel<DI, HP><<<grid, 256, 0, st>>>(p, chunk_rows);
   return cudaGetLastError();
 }
@@ -1115,17 +1332,14 @@ cudaError_t launch_wide_for(const SelectParams& p, int chunk, int chunk_rows, in
 #undef QSA_WIDE
 }
 
-// One row per sequence fills a tile of four rows at most: the narrowest tile that holds all
-// heads.  Otherwise 64 columns.
+// The narrowest tile that holds all heads of a row per thread: four rows (eight of one head).
 template <int DI>
 cudaError_t launch_score_for(SelectParams& p, int num_sms, cudaStream_t st) {
-  const bool narrow = p.cu == nullptr || p.Tq <= 4 * p.B;
-  const int groups = p.Hi > 16 ? (p.Hi + 15) / 16 : 1;
-  if (p.Hi > 8) return launch_score<DI, 16, 8>(p, groups, num_sms, st);
-  if (p.Hi > 4) return narrow ? launch_score<DI, 8, 4>(p, 1, num_sms, st) : launch_score<DI, 8, 8>(p, 1, num_sms, st);
-  if (p.Hi > 2) return narrow ? launch_score<DI, 4, 2>(p, 1, num_sms, st) : launch_score<DI, 4, 8>(p, 1, num_sms, st);
-  if (p.Hi > 1) return narrow ? launch_score<DI, 2, 1>(p, 1, num_sms, st) : launch_score<DI, 2, 8>(p, 1, num_sms, st);
-  return narrow ? launch_score<DI, 1, 1>(p, 1, num_sms, st) : launch_score<DI, 1, 8>(p, 1, num_sms, st);
+  if (p.Hi > 8) return launch_score<DI, 16, 8>(p, (p.Hi + 15) / 16, num_sms, st);
+  if (p.Hi > 4) return launch_score<DI, 8, 4>(p, 1, num_sms, st);
+  if (p.Hi > 2) return launch_score<DI, 4, 2>(p, 1, num_sms, st);
+  if (p.Hi > 1) return launch_score<DI, 2, 1>(p, 1, num_sms, st);
+  return launch_score<DI, 1, 1>(p, 1, num_sms, st);
 }
 
 // Many rows: small thread blocks, of which an SM holds many.  A row or a few per SM (a decode
@@ -1140,12 +1354,23 @@ cudaError_t launch_choose_for(const SelectParams& p, size_t smem, cudaStream_t s
 }
 
 cudaError_t launch_choose(SelectParams& p, int num_sms, cudaStream_t st) {
+  const int rows = p.c1 - p.c0;
+  // (with few rows the four warps of a block each would leave most of the device idle)
+  if (p.ld <= kPickKeys && p.top <= kPickKeys && rows > 2 * num_sms) {
+    p.cap = int((p.ld + 127) / 128 * 128);
+    const size_t smem = size_t(kPickWarps) * (p.cap + (p.top + 3) / 4 * 4) * 4;
+    const cudaError_t e = cudaFuncSetAttribute(qsa_select_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               int(smem));
+    if (e != cudaSuccess) return e;
+    qsa_select_pick_kernel<<<(rows + kPickWarps - 1) / kPickWarps, 32 * kPickWarps, smem, st>>>(p);
+    return cudaGetLastError();
+  }
   // room for what the sample's border lets through: about 1.3 to 2 times `top` for long rows
   const int want = p.top * 5 / 2 > 2048 ? p.top * 5 / 2 : 2048;
-  p.cap = int(p.ld < want ? (p.ld < kSample ? kSample : p.ld) : want) / 4 * 4;
+  p.cap = int(p.ld < want ? (p.ld < kSample ? kSample : p.ld) : want);
+  p.cap = (p.cap + 127) / 128 * 128;
   p.window = p.ld / 32 < kWindow ? int(p.ld / 32) : kWindow;  // (ld is a multiple of 32)
   const size_t smem = size_t(p.cap) * (p.ld > p.cap ? 8 : 4) + size_t(p.top + 3) / 4 * 16 + size_t(p.window) * 8;
-  const int rows = p.c1 - p.c0;
   return rows > 2 * num_sms ? launch_choose_for<128>(p, smem, st)
          : rows > num_sms   ? launch_choose_for<256>(p, smem, st)
                             : launch_choose_for<1024>(p, smem, st);
@@ -1235,6 +1460,7 @@ extern "C" qsa_status_t qsa_select_slots(
   const int64_t ld = lay.ld;
   const int32_t rows = lay.rows;
   const bool wide = use_wide(Tq, B, Hi, cu_q != nullptr);
+  if (ld >= (1 << 30)) QSA_REJECT(QSA_ERR_UNSUPPORTED, "a page table of %lld blocks", (long long)ld);
   const size_t need = cu_q != nullptr ? lay.bytes : lay.tiles;
   if (need > 0 && (workspace == nullptr || workspace_bytes < need))
     QSA_REJECT(QSA_ERR_WORKSPACE, "workspace of %zu bytes needed, got %zu", need,
@@ -1252,7 +1478,7 @@ extern "C" qsa_status_t qsa_select_slots(
   p.scales = scales;
   p.table = page_table, p.lens = seq_lens, p.cu = cu_q;
   p.out = slot_idx, p.width = width;
-  p.keys = static_cast<uint32_t*>(workspace);
+  p.scores = static_cast<float*>(workspace);
   p.tiles = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + lay.tiles);
   p.tile_q = static_cast<uint8_t*>(workspace) + lay.tile_q;
   p.err_word = err_word;
