@@ -138,10 +138,10 @@ def test_decode_plan(B, Hq, Hkv, P, page, request_, fp8):
 def test_select_workspace_is_bounded():
     assert qsa.qsa_select_slots_workspace_bytes(0, 4, 16, 64, 4, 128, 4) == 0
     assert qsa.qsa_select_slots_workspace_bytes(1, 1, 16, 64, 4, 128, 4) == 256 * 4
-    # keys of a chunk of rows: 64 MiB while 64 rows fit; codes and gains of 256 columns per tile of rows
+    # scores of a chunk of rows: 512 MiB while 64 rows fit; codes and gains of 256 columns per tile of rows
     n = qsa.qsa_select_slots_workspace_bytes(1 << 16, 1, 1024, 64, 4, 128, 4)
-    tiles = 64 * (1024 // 64 + 1)
-    assert n == (64 << 20) + tiles * (16 + 256 * 132)
+    tiles = 8 * (8192 // 64 + 1)
+    assert n == (512 << 20) + (tiles * 16 + 255) // 256 * 256 + tiles * 256 * 132
     for bad in ((1, 1, 16, 62, 4, 128, 4), (1, 1, 16, 64, 0, 128, 4), (1, 1, 16, 64, 4, 96, 4)):
         with pytest.raises(qsa.QSAError):
             qsa.qsa_select_slots_workspace_bytes(*bad)

@@ -118,13 +118,40 @@ __device__ __forceinline__ uint64_t clock_ns() {
 }
 
 // Waits for a phase of an mbarrier, one second at most; false when it has not come by then.
-// (64 polls between two looks at the clock.)
+// The hint lets the hardware hold the thread for up to 100 us, or until the phase completes,
+// instead of a few cycles: waiting warps would otherwise take issue slots from working ones.
+__device__ __forceinline__ bool poll_phase(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n  .reg .pred p;\n  mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      "  selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity), "r"(100000u)
+      : "memory");
+  return done != 0;
+}
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity) {
-  if (mbar_wait(bar, parity, 64)) return true;
+  if (poll_phase(bar, parity)) return true;
   const uint64_t start = clock_ns();
-  while (clock_ns() - start < 1000000000u)
-    if (mbar_wait(bar, parity, 64)) return true;
+  do {
+    if (poll_phase(bar, parity)) return true;
+  } while (clock_ns() - start < 1000000000u);
   return false;
+}
+
+// The same without suspending the thread: for waits on a pipeline's critical path.
+__device__ __forceinline__ bool spin_phase(uint32_t bar, uint32_t parity) {
+  for (uint32_t n = 0;; ++n) {
+    uint32_t done;
+    asm volatile(
+        "{\n  .reg .pred p;\n  mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "  selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if (n == 4096) return wait_phase(bar, parity);
+  }
 }
 
 // Bulk copy from this device's memory to shared memory, completing on an mbarrier; both

@@ -2,10 +2,9 @@
 // sequence and the choice of the row's slots.  Contract: include/qsa_layer.h
 // (qsa_select_slots).
 //
-// Two kernels over chunks of rows: the score kernel writes an order-preserving 32-bit key
-// per (row, block) into the workspace, the choice kernel finds each row's top_blocks-th
-// largest key by radix passes and writes the slots of the blocks above it.  A chunk's keys
-// are at most kChunkBytes, so they stay in the 126 MB L2 between the two kernels.
+// Two kernels over chunks of rows: the score kernel writes a 32-bit score per (row, block)
+// into the workspace, the choice kernel finds the border of each row's top_blocks best and
+// writes the slots of the blocks above it.
 #include "qsa_layer.cuh"
 
 namespace {
@@ -15,7 +14,7 @@ using namespace qsa;
 constexpr int kKeyTile = 128;                 // micro-blocks per tile
 constexpr int kScoreThreads = 256;
 constexpr int kScoreBlocks = 2;               // of an SM
-constexpr int64_t kChunkBytes = 64 << 20;     // keys of one chunk of rows
+constexpr int64_t kChunkBytes = 512 << 20;    // most scores of one chunk of rows
 constexpr int kMinChunkRows = 64;
 
 struct SelectParams {
@@ -32,7 +31,7 @@ struct SelectParams {
   int32_t Tq, B, P, page_size, per_page, Hi, block, top, sink, local;
   int4* tiles;         // tcgen05 form: tiles of rows [chunks, max_tiles], and their codes and gains
   uint8_t* tile_q;
-  int32_t cap, window;              // keys of a row, and words of its marks, in the choice's shared memory
+  int32_t cap, queue, window;              // keys of a row, and words of its marks, in the choice's shared memory
   uint32_t page_magic, block_magic; // 2^32 / per_page (/ block), rounded up
 };
 
@@ -341,10 +340,9 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks)
 // within a thread, two rows per packed instruction.
 constexpr int kWideCols = 256;
 constexpr int kWideStages = 6;                     // key tiles in shared memory
-constexpr int kWideQ = 3;                          // Q tiles in shared memory (one more than a producer's lag)
-constexpr int kWideLag = 2;                        // tiles a producer has in flight behind the one it issues
+constexpr int kWideQ = 3;                          // Q tiles in shared memory (see the producers)
 constexpr int kPrepParts = 4;                      // thread blocks that make a tile's codes
-constexpr int kEpilogueWarps = 16, kProducerWarps = 4;
+constexpr int kEpilogueWarps = 16, kGroupWarps = 4, kProducerWarps = 2 * kGroupWarps;
 constexpr int kWideThreads = 32 * (kEpilogueWarps + kProducerWarps + 1);
 
 __host__ __device__ constexpr int wide_tile_bytes(int DI) { return kWideCols * (DI + 4); }  // codes, then gains
@@ -512,7 +510,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   }
   if (tid == 0) {
     for (int i = 0; i < kWideStages; ++i) {
-      mbar_init(bar(kFull + i), 32 * kProducerWarps);
+      mbar_init(bar(kFull + i), 32 * kGroupWarps);
       mbar_init(bar(kFree + i), 1 + kEpilogueWarps);
     }
     for (int i = 0; i < kWideQ; ++i) {
@@ -536,13 +534,27 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   const int tile0 = sStart[0], first_kt = sStart[1];
   const int share = int(u1 - u0);
   bool late = false;
+  int q_loaded = -1;  // (the first thread of a producer group) the last Q tile it loaded
 
   if (warp >= kEpilogueWarps && warp < kEpilogueWarps + kProducerWarps) {
-    // ---- producers: one key row per thread -----------------------------------------------------
-    const int r = tid - 32 * kEpilogueWarps;
-    int tile = tile0, kt = first_kt, qn = 0;  // qn: Q tiles issued
+    // ---- producers: two groups take the key tiles in turn, one key row per thread ----------------
+    // A group hands tile i over once it has issued tile i + 2.  So when it waits for the Q tile
+    // three before the one it is about to load, whose last key tile is i - 3 or earlier, both
+    // groups have handed over all that the wait depends on, or will without waiting for this.
+    const int group = (warp - kEpilogueWarps) / kGroupWarps, r = tid - 32 * (kEpilogueWarps + group * kGroupWarps);
+    int tile = tile0, kt = first_kt, qn = 0;  // qn: the Q tile's number within this block
     bool new_q = true;
     int4 w = tiles[tile];
+    auto advance = [&]() {
+      new_q = false;
+      if (++kt == tile_units(w.w)) {
+        kt = 0;
+        new_q = true;
+        ++qn;
+        do ++tile; while (tile < max_tiles && tiles[tile].w == 0);
+        if (tile < max_tiles) w = tiles[tile];
+      }
+    };
     // of this thread's row of key tile kt of w: the page as the table has it, the block within
     // it, and whether there is such a block (used one step later, when the load has arrived)
     int page = -1, off = 0;
@@ -559,34 +571,31 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       off = j - m * p.per_page;
       page = __ldg(p.table + w.x * p.table_st + m);
     };
+    if (group == 1 && share > 1) advance();
     lookup();
     const uint32_t row_s = smem_addr(smem) + (r >> 3) * 256 + (r & 7) * 16;
-    for (int i = 0; i < share; ++i) {
+    int issued = 0;
+    for (int i = group; i < share; i += 2, ++issued) {
       const bool ok = live && page >= 0 && page < p.pages, bad = live && !ok;
       const int64_t phys = ok ? int64_t(page) * p.per_page + off : 0;
       const bool load_q = new_q;
-      const int this_tile = tile;
-      new_q = false;
-      if (++kt == tile_units(w.w)) {
-        kt = 0;
-        new_q = true;
-        do ++tile; while (tile < max_tiles && tiles[tile].w == 0);
-        if (tile < max_tiles) w = tiles[tile];
+      const int this_tile = tile, this_q = qn;
+      if (i + 1 < share) advance();
+      if (i + 2 < share) {
+        advance();
+        lookup();
       }
-      if (i + 1 < share) lookup();
       const int stage = i % kWideStages;
       if (i >= kWideStages && !wait_phase(bar(kFree + stage), (i / kWideStages - 1) & 1)) late = true;
-      if (load_q) {
-        const int qb = qn % kWideQ;
-        if (r == 0 && !late) {
-          if (qn >= kWideQ && !wait_phase(bar(kQFree + qb), (qn / kWideQ - 1) & 1)) late = true;
-          if (!late) {
-            mbar_arrive_expect_tx(bar(kQFull + qb), C::kQBytes);
-            bulk_copy(smem_addr(sQ) + qb * C::kQBytes, tile_q + int64_t(this_tile) * C::kQBytes, C::kQBytes,
-                      bar(kQFull + qb));
-          }
+      if (load_q && r == 0 && !late) {
+        const int qb = this_q % kWideQ;
+        if (this_q >= kWideQ && !wait_phase(bar(kQFree + qb), (this_q / kWideQ - 1) & 1)) late = true;
+        if (!late) {
+          mbar_arrive_expect_tx(bar(kQFull + qb), C::kQBytes);
+          bulk_copy(smem_addr(sQ) + qb * C::kQBytes, tile_q + int64_t(this_tile) * C::kQBytes, C::kQBytes,
+                    bar(kQFull + qb));
+          q_loaded = this_q;
         }
-        if (!late) ++qn;
       }
       if (late) break;
       if (bad && p.err_word != nullptr) atomicOr(p.err_word, QSA_ERRBIT_SLOT_RANGE);
@@ -602,18 +611,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       else
         sScale[stage * kKeyTile + r] = __int_as_float(0x7fffffff);
       cp_async_commit();
-      if (i >= kWideLag) {  // the tile issued kWideLag before has landed: hand it over
-        cp_async_wait<kWideLag>();
+      if (issued >= 1) {  // the group's tile before has landed: hand it over
+        cp_async_wait<1>();
         fence_proxy_async_smem();
-        mbar_arrive(bar(kFull + (i - kWideLag) % kWideStages));
+        mbar_arrive(bar(kFull + (i - 2) % kWideStages));
       }
     }
     cp_async_wait<0>();
     fence_proxy_async_smem();
-    if (!late)
-      for (int i = max(share - kWideLag, 0); i < share; ++i) mbar_arrive(bar(kFull + i % kWideStages));
-    if (r == 0)  // no copy in flight
-      for (int i = max(qn - kWideQ, 0); i < qn; ++i) late |= !wait_phase(bar(kQFull + i % kWideQ), (i / kWideQ) & 1);
+    if (!late && issued > 0) mbar_arrive(bar(kFull + (group + 2 * (issued - 1)) % kWideStages));
   } else if (warp == kEpilogueWarps + kProducerWarps) {
     // ---- one thread issues the MMAs ------------------------------------------------------------
     if (lane == 0) {
@@ -661,13 +667,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const int r = quad * 32 + lane;
     constexpr int kPartRows = kPartCols / HP;
     int tile = tile0, kt = first_kt, qn = 0;
+    bool new_q = true;
     int4 w = tiles[tile];
     for (int i = 0; i < share; ++i) {
       const int stage = i % kWideStages, acc = i & 1;
       // (the key stage and the Q tile landed before their product: these waits order the reads)
-      bool here = wait_phase(bar(kAccFull + acc), (i >> 1) & 1);
-      here = here && wait_phase(bar(kFull + stage), (i / kWideStages) & 1) &&
-             wait_phase(bar(kQFull + qn % kWideQ), (qn / kWideQ) & 1);
+      bool here = wait_phase(bar(kFull + stage), (i / kWideStages) & 1);
+      if (new_q) here = here && wait_phase(bar(kQFull + qn % kWideQ), (qn / kWideQ) & 1);
+      new_q = false;
+      here = here && wait_phase(bar(kAccFull + acc), (i >> 1) & 1);
       if (__any_sync(0xffffffffu, !here)) {
         late = true;
         break;
@@ -722,14 +730,19 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         if (lane == 0) mbar_arrive(bar(kQFree + qn % kWideQ));
         ++qn;
         kt = 0;
+        new_q = true;
         do ++tile; while (tile < max_tiles && tiles[tile].w == 0);
         if (tile < max_tiles) w = tiles[tile];
       }
     }
   }
-  if (late && p.err_word != nullptr) atomicOr(p.err_word, QSA_ERRBIT_TIMEOUT);
+  // (every Q tile's copy has landed when its product was issued, unless a wait ran out)
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  __syncthreads();
+  if (__syncthreads_or(late)) {
+    if (late && p.err_word != nullptr) atomicOr(p.err_word, QSA_ERRBIT_TIMEOUT);
+    if (q_loaded >= 0) wait_phase(bar(kQFull + q_loaded % kWideQ), (q_loaded / kWideQ) & 1);  // a second chance
+    __syncthreads();
+  }
   if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }
 
@@ -1054,8 +1067,8 @@ template <int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : THREADS == 256 ? 4 : 1) qsa_select_choose_kernel(const SelectParams p) {
   constexpr int kBatch = THREADS == 1024 ? 4 : 2;  // 16-byte loads of keys per thread and step
   extern __shared__ __align__(16) uint32_t dyn[];
-  uint32_t* sKey = dyn;                                       // [cap]
-  int* sIdx = reinterpret_cast<int*>(sKey + p.cap);           // [cap], absent when every row fits
+  uint32_t* sKey = dyn;  // [cap], and room for `queue` 16-bit numbers before the keys are there
+  int* sIdx = reinterpret_cast<int*>(sKey + max(p.cap, p.ld > p.cap ? p.queue / 2 : 0));  // [cap], absent when every row fits
   int* sList = sIdx + (p.ld > p.cap ? p.cap : 0);             // [top] first slot of each taken block, or -1
   __shared__ __align__(16) ChooseShared sh;
   uint32_t* sOver = reinterpret_cast<uint32_t*>(sList + (p.top + 3) / 4 * 4);  // [window] each
@@ -1123,68 +1136,80 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : THREADS == 256 
       const float hits = float(want) * kSample / float(f);
       int rank = min(int(hits + 4.f * sqrtf(hits)) + 4, kSample);
       uint32_t low = kth_largest<THREADS, false>(kSample, rank, in_list, sh).key;
-      // The blocks of keys from `low` up.  More than there is room for: the want-th largest of
-      // those that had room is a better border, since as many keys as wanted reach it.  Fewer
-      // than wanted, or no better border: every block of the row is searched.
+      // The blocks of keys from `low` up: every lane queues the ones it meets (16-bit numbers, in
+      // the keys' room), a scan over the lanes then puts the queues together.  More than there
+      // is room for: the want-th largest of those that had room is a better border, since as
+      // many keys as wanted reach it.  Fewer than wanted, or no better border: every block of
+      // the row is searched.
+      uint16_t* queue = reinterpret_cast<uint16_t*>(sKey);
+      const int longest = p.queue / THREADS;
+      constexpr int kStep = THREADS * kBatch;  // 16-byte loads of a step
       for (int tries = 0; tries < 3; ++tries) {
         __syncthreads();
         if (tid == 0) sh.n = 0;
         __syncthreads();
         const float least = key_score(low);
-        uint4 raw[kBatch], next[kBatch];
-        auto load = [&](int i0) {
+        int have = 0, all = 0;
+        for (int s0 = 0; s0 * 4 < f; s0 += kStep * (65536 / (4 * kBatch))) {
+          const int s1 = int(min(int64_t(s0) + kStep * (65536 / (4 * kBatch)), int64_t(f + 3) / 4));
+          uint4 raw[kBatch], next[kBatch];
+          auto load = [&](int i0) {
 #pragma unroll
-          for (int u = 0; u < kBatch; ++u) {
-            next[u] = make_uint4(0u, 0u, 0u, 0u);
-            if ((i0 + lane + u * THREADS) * 4 < f) next[u] = __ldg(row4 + i0 + lane + u * THREADS);
-          }
-        };
-        load(warp * 32);
-        for (int i0 = warp * 32; i0 * 4 < f; i0 += THREADS * kBatch) {
+            for (int u = 0; u < kBatch; ++u) {
+              next[u] = make_uint4(0u, 0u, 0u, 0u);
+              if ((i0 + lane + u * THREADS) * 4 < f) next[u] = __ldg(row4 + i0 + lane + u * THREADS);
+            }
+          };
+          load(s0 + warp * 32);
+          int mine = 0, number = 0;
+          for (int i0 = s0 + warp * 32; i0 < s1; i0 += kStep, number += 4 * kBatch) {
 #pragma unroll
-          for (int u = 0; u < kBatch; ++u) raw[u] = next[u];
-          load(i0 + THREADS * kBatch);
-          float k[4 * kBatch];
-          uint32_t keep = 0u;  // a bit per score of this lane
+            for (int u = 0; u < kBatch; ++u) raw[u] = next[u];
+            if (i0 + kStep < s1) load(i0 + kStep);
+            float k[4 * kBatch];
+            uint32_t keep = 0u;  // a bit per score of this lane
 #pragma unroll
-          for (int u = 0; u < kBatch; ++u)
-            k[4 * u] = __uint_as_float(raw[u].x), k[4 * u + 1] = __uint_as_float(raw[u].y),
-            k[4 * u + 2] = __uint_as_float(raw[u].z), k[4 * u + 3] = __uint_as_float(raw[u].w);
-          if (i0 * 4 >= p.sink && (i0 + 32 + (kBatch - 1) * THREADS) * 4 <= f - p.local) {
+            for (int u = 0; u < kBatch; ++u)
+              k[4 * u] = __uint_as_float(raw[u].x), k[4 * u + 1] = __uint_as_float(raw[u].y),
+              k[4 * u + 2] = __uint_as_float(raw[u].z), k[4 * u + 3] = __uint_as_float(raw[u].w);
+            if (i0 * 4 >= p.sink && (i0 + 32 + (kBatch - 1) * THREADS) * 4 <= f - p.local) {
 #pragma unroll
-            for (int x = 0; x < 4 * kBatch; ++x) keep_bit(keep, k[x], least, 1u << x);
-          } else {
+              for (int x = 0; x < 4 * kBatch; ++x) keep_bit(keep, k[x], least, 1u << x);
+            } else {
 #pragma unroll
-            for (int x = 0; x < 4 * kBatch; ++x) {
-              const int j = (i0 + lane + (x >> 2) * THREADS) * 4 + (x & 3);
-              keep |= j < f && !forced(j) && k[x] >= least ? 1u << x : 0u;
+              for (int x = 0; x < 4 * kBatch; ++x) {
+                const int j = (i0 + lane + (x >> 2) * THREADS) * 4 + (x & 3);
+                keep |= j < f && !forced(j) && k[x] >= least ? 1u << x : 0u;
+              }
+            }
+            while (keep != 0u) {
+              const int x = __ffs(keep) - 1;
+              keep &= keep - 1;
+              if (mine < longest) queue[mine * THREADS + tid] = uint16_t(number + x);
+              ++mine;
             }
           }
-          const int mine = __popc(keep);
-          int at = mine;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, at, o);
-            if (lane >= o) at += y;
+          all += mine;
+          const int kept = min(mine, longest);
+          int total;
+          int at = have + block_scan<THREADS>(kept, sTmp, total) - kept;
+          for (int i = 0; i < kept && at < p.cap; ++i, ++at) {
+            const int v = queue[i * THREADS + tid], x = v % (4 * kBatch);
+            sIdx[at] = (s0 + v / (4 * kBatch) * kStep + warp * 32 + lane + (x >> 2) * THREADS) * 4 + (x & 3);
           }
-          int before = 0;
-          if (lane == 31 && at > 0) before = atomicAdd(&sh.n, at);
-          at += __shfl_sync(0xffffffffu, before, 31) - mine;
-          while (keep != 0u) {
-            const int x = __ffs(keep) - 1;
-            keep &= keep - 1;
-            if (at < p.cap) sIdx[at] = (i0 + lane + (x >> 2) * THREADS) * 4 + (x & 3);
-            ++at;
-          }
+          have += total;
+          __syncthreads();  // (the queues)
         }
+        all = int(__reduce_add_sync(0xffffffffu, unsigned(all)));
+        if (lane == 0) atomicAdd(&sh.n, all);
         __syncthreads();
-        const int n = sh.n, room = min(n, p.cap);
-        if (n < want) break;
+        const int n = sh.n, room = min(have, p.cap);
+        if (room < want) break;
 #pragma unroll 4
         for (int i = tid; i < room; i += THREADS) sKey[i] = order_key(__float_as_uint(__ldg(row + sIdx[i])));
         border = kth_largest<THREADS, true>(room, want, in_list, sh);
         if (n == room) listed = n;
-        if (n == room || border.key == low) break;
+        if (n == room || border.key <= low) break;
         low = border.key;
       }
       if (listed < 0) border = kth_largest<THREADS, true>(f, want, in_row, sh);
@@ -1256,12 +1281,17 @@ int64_t blocks_ld(int32_t P, int32_t page_size, int32_t block) {
   return (n + 31) / 32 * 32;
 }
 
-// Rows of a chunk: as many as kChunkBytes of keys hold, at least kMinChunkRows.
+// Rows of a chunk: as many as kChunkBytes of scores hold, at least kMinChunkRows, and the
+// chunks as equal as they can be.  (Chunks that stay in the 126 MB L2 between the kernels cost
+// more in the ends of their launches than they save: 7,810 rows of 16,384 blocks took 583 us
+// in chunks of 64 MB, 556 of 128, 527 of 192, 460 in one piece.)
 int32_t chunk_rows(int32_t Tq, int64_t ld) {
   int64_t n = ld > 0 ? kChunkBytes / (ld * 4) : Tq;
   n = n < kMinChunkRows ? kMinChunkRows : n;
   if (ld > 0 && n * ld >= (1 << 30)) n = ((1 << 30) - 1) / ld;
-  return int32_t(n < Tq ? n : Tq);
+  if (n < 1) return 0;
+  const int64_t chunks = (int64_t(Tq) + n - 1) / n;
+  return chunks > 0 ? int32_t((int64_t(Tq) + chunks - 1) / chunks) : 0;
 }
 
 template <int DI, int HP, int NT>
@@ -1366,11 +1396,15 @@ cudaError_t launch_choose(SelectParams& p, int num_sms, cudaStream_t st) {
     return cudaGetLastError();
   }
   // room for what the sample's border lets through: about 1.3 to 2 times `top` for long rows
-  const int want = p.top * 5 / 2 > 2048 ? p.top * 5 / 2 : 2048;
+  const int want = p.top * 5 / 2 > 1536 ? p.top * 5 / 2 : 1536;
   p.cap = int(p.ld < want ? (p.ld < kSample ? kSample : p.ld) : want);
   p.cap = (p.cap + 127) / 128 * 128;
   p.window = p.ld / 32 < kWindow ? int(p.ld / 32) : kWindow;  // (ld is a multiple of 32)
-  const size_t smem = size_t(p.cap) * (p.ld > p.cap ? 8 : 4) + size_t(p.top + 3) / 4 * 16 + size_t(p.window) * 8;
+  const int threads = rows > 2 * num_sms ? 128 : rows > num_sms ? 256 : 1024;
+  // a lane's queue: at least 24 entries (about 8 are expected of 128 lanes, fewer of more)
+  p.queue = 2 * p.cap > 24 * threads ? 2 * p.cap / (2 * threads) * (2 * threads) : 24 * threads;
+  const size_t keys = p.ld > p.cap ? size_t(p.cap > p.queue / 2 ? p.cap : p.queue / 2) + p.cap : size_t(p.cap);
+  const size_t smem = keys * 4 + size_t(p.top + 3) / 4 * 16 + size_t(p.window) * 8;
   return rows > 2 * num_sms ? launch_choose_for<128>(p, smem, st)
          : rows > num_sms   ? launch_choose_for<256>(p, smem, st)
                             : launch_choose_for<1024>(p, smem, st);
