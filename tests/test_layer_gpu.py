@@ -707,3 +707,26 @@ def test_select_many_short_rows_of_several_sequences():
     c["page_table"][2, 5], c["scales"][::3] = -1, float("nan")
     assert check_select(c, 40) == SLOT_RANGE
     assert check_select(c, 300) == SLOT_RANGE
+
+
+def test_calls_that_read_what_the_call_before_wrote():
+    """Back to back on one stream, nothing between: every call's inputs are the outputs of the one
+    before it, with and without scores to compute."""
+    c = select_case(94, [900, 5, 2001, 77], None, 4, 128, 4, 64)
+    base = run_select(c, 40)[1]
+    torch.cuda.synchronize()
+    for top in (40, 600):  # 600 blocks: more than the table holds, nothing is scored
+        steps, lens = [], c["seq_lens"]
+        for _ in range(12):
+            idx, width = run_select(dict(c, seq_lens=lens), top)
+            steps.append((lens, idx, width))
+            lens = width
+        torch.cuda.synchronize()
+        for lens, idx, width in steps:
+            want = ref.select(c["q"], c["weight"], c["codes"], c["scales"], c["page_table"], lens, None, top, 64, 4, 0, 0)
+            assert torch.equal(idx.cpu(), torch.from_numpy(want[0])) and torch.equal(width.cpu(), torch.from_numpy(want[1]))
+    d = decode_case(95, [900, 5, 2001, 77], 16, 2, 64)
+    d["seq_lens"] = run_select(c, 40)[1]  # the selection's widths as lengths
+    out = qsa.paged_decode(**d)
+    want, tol, _ = ref.paged_decode(d["q"], d["k_cache"], d["v_cache"], d["page_table"], base, 64, 1 / 16)
+    close(out, want, tol)

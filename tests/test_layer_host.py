@@ -125,9 +125,9 @@ def test_decode_refusals(lib, change, status):
 @pytest.mark.parametrize("fp8", [False, True])
 def test_decode_plan(B, Hq, Hkv, P, page, request_, fp8):
     n, ws = qsa.qsa_paged_decode_plan(B, Hq, Hkv, 256, P, page, fp8, 148, request_)
-    # a block per KV head in every group; no group without a unit of 64 tokens at the
-    # sequences' greatest length
-    assert n % Hkv == 0 and Hkv <= n <= Hkv * max(1, B * -(-P * page // 64))
+    # a block per KV head in every group; no group without a unit of tokens at the sequences'
+    # greatest length
+    assert n % Hkv == 0 and Hkv <= n <= Hkv * max(1, B * -(-P * page // (64 if fp8 else 32)))
     if request_:
         assert n <= max(request_, Hkv)
     assert ws == 0 if n == Hkv else ws >= n * 2 * (Hq // Hkv) * 257 * 4

@@ -9,7 +9,6 @@ using namespace qsa;
 constexpr int kD = kHeadDim;
 constexpr int kStages = 2;
 constexpr int kSub = 16;                 // slots of a warp's sub-tile (the M of one MMA)
-constexpr int kUnit = 64;                // slots that the work is shared out in
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kRescaleLog2 = 8.0f;
 
@@ -24,6 +23,7 @@ struct DecodeParams {
   uint32_t k_ss, v_ss;  // bytes
   int64_t k_sh, v_sh;   // bytes
   int32_t B, Hq, Hkv, G, P, page_size;
+  int32_t unit, unit_log2;  // slots that the work is shared out in: a sub-tile for each warp of a block
   uint32_t page_magic;  // 2^32 / page_size, rounded up
   float scale_log2, v_scale;
 };
@@ -35,7 +35,7 @@ __device__ __forceinline__ int tokens_of(const DecodeParams& p, int b, bool repo
   return int(min(int64_t(max(n, 0)), most));
 }
 
-__device__ __forceinline__ int units_of(int len) { return (len + kUnit - 1) / kUnit; }
+__device__ __forceinline__ int units_of(const DecodeParams& p, int len) { return (len + p.unit - 1) >> p.unit_log2; }
 
 // The work: the units of all sequences in order, cut into `groups` shares whose sizes differ
 // by one at most.  Group c's Hkv thread blocks take the same share of one KV head each, side
@@ -66,7 +66,7 @@ __device__ __forceinline__ Share share_of(int64_t total, int groups) {
 __device__ __forceinline__ int64_t units_before(const DecodeParams& p, int b, int64_t& all, bool report) {
   int64_t mine = 0, before = 0;
   for (int i = threadIdx.x & 31; i < p.B; i += 32) {
-    const int n = units_of(tokens_of(p, i, report));
+    const int n = units_of(p, tokens_of(p, i, report));
     mine += n;
     before += i < b ? n : 0;
   }
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(Decode<FP8, NT>::kThreads) qsa_paged_decode_ke
   __shared__ float2 sState[kWarps][NT * 8];  // (m, l) of each warp and head
   uint8_t* sQ = smem + C::kRing;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the join waits for this grid's end)
+  begin_kernel();
   int64_t total;
   units_before(p, 0, total, blockIdx.x == 0 && warp == 0);
   // sequences without a token: zeros
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(Decode<FP8, NT>::kThreads) qsa_paged_decode_ke
   int b = 0;
   int64_t seg0 = 0;  // its first unit
   for (;; b += 32) {
-    const int64_t n = b + lane < p.B ? int64_t(units_of(tokens_of(p, b + lane, false))) : 0;
+    const int64_t n = b + lane < p.B ? int64_t(units_of(p, tokens_of(p, b + lane, false))) : 0;
     int64_t to = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(Decode<FP8, NT>::kThreads) qsa_paged_decode_ke
     }
     seg0 += __shfl_sync(0xffffffffu, to, 31);
   }
-  int len = tokens_of(p, b, false), units = units_of(len);
+  int len = tokens_of(p, b, false), units = units_of(p, len);
 
   const uint32_t ring = smem_addr(smem) + warp * kStages * C::kStageBytes;
   const uint32_t q_s = smem_addr(sQ);
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(Decode<FP8, NT>::kThreads) qsa_paged_decode_ke
   int stage = 0;
   for (int64_t u = u0; u < u1;) {
   const int64_t seg1 = seg0 + units, end = min(seg1, u1);
-  const int s0 = int(u - seg0) * kUnit, s1 = int(min(int64_t(len), (end - seg0) * kUnit));
+  const int s0 = int(u - seg0) * p.unit, s1 = int(min(int64_t(len), (end - seg0) * p.unit));
   const int h0 = j * p.G;
   const uint8_t* kg = p.k + j * p.k_sh;
   const uint8_t* vg = p.v + j * p.v_sh;
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(Decode<FP8, NT>::kThreads) qsa_paged_decode_ke
     seg0 = seg1;
     do ++b; while (tokens_of(p, b, false) == 0);
     len = tokens_of(p, b, false);
-    units = units_of(len);
+    units = units_of(p, len);
   }
   }
 }
@@ -468,13 +468,14 @@ __global__ void __launch_bounds__(THREADS) qsa_paged_join_kernel(const DecodePar
   __shared__ float sRed[THREADS / 32], sSum[kParts];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq, j = h / p.G, g = h - j * p.G;
-  const int units = units_of(tokens_of(p, b, false));
+  launch_next();
+  const int units = units_of(p, tokens_of(p, b, false));
   int64_t total;
   const int64_t seg0 = units_before(p, b, total, false), seg1 = seg0 + units;
   const Share share = share_of(total, groups);
   int first = 0, n = 0;
   if (units > 0) first = share.owner(seg0), n = share.owner(seg1 - 1) - first + 1;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_last();
   if (n <= 1) return;  // written whole
   // the first block's piece is its last unless it begins with it; the others begin with theirs
   const int shift = share.begin(first) < seg0 ? 1 : 0;
@@ -527,6 +528,8 @@ __global__ void __launch_bounds__(THREADS) qsa_paged_join_kernel(const DecodePar
     p.lse[int64_t(b) * p.Hq + h] = top == kNegInf ? kNegInf : top + fast_log2(l_all);
 }
 
+int decode_unit(int32_t kv_fp8) { return kSub * (kv_fp8 ? Decode<true, 1>::kWarps : Decode<false, 1>::kWarps); }
+
 struct DecodePlan {
   int32_t blocks;
   size_t lse_offset, bytes;
@@ -539,7 +542,8 @@ DecodePlan decode_plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t P, int32_t pa
                               : (G <= 8 ? Decode<false, 1>::kResident : Decode<false, 2>::kResident);
   // groups of a block per KV head; no more of them than there are units when every sequence
   // is as long as its pages
-  const int64_t most = int64_t(B) * ((int64_t(P) * page_size + kUnit - 1) / kUnit);
+  const int unit = decode_unit(kv_fp8);
+  const int64_t most = int64_t(B) * ((int64_t(P) * page_size + unit - 1) / unit);
   int64_t n = (request > 0 ? request : int64_t(num_sms > 0 ? num_sms : 1) * resident) / Hkv;
   n = n > most ? most : n;
   n = n < 1 ? 1 : n;
@@ -573,23 +577,12 @@ cudaError_t launch_decode(const DecodeParams& p, int blocks, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(qsa_paged_decode_kernel<FP8, NT>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::kSmem));
   if (e != cudaSuccess) return e;
-  qsa_paged_decode_kernel<FP8, NT><<<blocks, C::kThreads, C::kSmem, st>>>(p);
-  return cudaGetLastError();
+  return launch(qsa_paged_decode_kernel<FP8, NT>, blocks, C::kThreads, C::kSmem, st, p);
 }
 
-// Launched while the decode kernel still runs: its blocks wait for that grid's end.
 template <int THREADS>
 cudaError_t launch_join(const DecodeParams& p, int groups, cudaStream_t st) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(p.B) * p.Hq);
-  cfg.blockDim = dim3(THREADS);
-  cfg.stream = st;
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, qsa_paged_join_kernel<THREADS>, p, groups);
+  return launch(qsa_paged_join_kernel<THREADS>, unsigned(p.B) * p.Hq, THREADS, 0, st, p, groups);
 }
 
 }  // namespace
@@ -664,6 +657,8 @@ extern "C" qsa_status_t qsa_paged_decode(
   p.k_ss = uint32_t(k_stride_s * e), p.k_sh = k_stride_h * e;
   p.v_ss = uint32_t(v_stride_s * e), p.v_sh = v_stride_h * e;
   p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv, p.P = P, p.page_size = page_size;
+  p.unit = decode_unit(kv_fp8);
+  for (p.unit_log2 = 0; (1 << p.unit_log2) < p.unit;) ++p.unit_log2;
   p.page_magic = uint32_t(((uint64_t(1) << 32) + page_size - 1) / page_size);
   // log2(e): the softmax runs in base 2
   p.scale_log2 = (kv_fp8 ? scale * k_scale : scale) * 1.4426950408889634f;

@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 5) qsa_norm_rope_kernel(const
   __shared__ float2 sTurn[kRopeWarps][kMaxPairs];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t unit = int64_t(blockIdx.x) * kRopeWarps + warp;
+  begin_kernel();
   if (unit >= p.units) return;
   const int t = p.parts == 1 ? int(unit) : int(unit / p.parts);
   const int first = int(unit - int64_t(t) * p.parts) * p.steps;
@@ -243,6 +244,7 @@ constexpr int kPackThreads = 128;
 template <int DI>
 __global__ void __launch_bounds__(kPackThreads) qsa_pack_index_kernel(const PackParams p) {
   constexpr int kLanes = DI / 8;
+  begin_kernel();
   const int64_t i = (int64_t(blockIdx.x) * kPackThreads + threadIdx.x) / kLanes;
   const int l = threadIdx.x % kLanes;
   int64_t b = -1;
@@ -400,10 +402,10 @@ extern "C" qsa_status_t qsa_qk_norm_rope(
   const int64_t grid = (p.units + kRopeWarps - 1) / kRopeWarps;
   if (grid > INT32_MAX) QSA_REJECT(QSA_ERR_UNSUPPORTED, "%lld thread blocks in one launch", (long long)grid);
   const auto st = static_cast<cudaStream_t>(stream);
-  if (D == 256) qsa_norm_rope_kernel<256><<<unsigned(grid), 32 * kRopeWarps, 0, st>>>(p);
-  else if (D == 128) qsa_norm_rope_kernel<128><<<unsigned(grid), 32 * kRopeWarps, 0, st>>>(p);
-  else qsa_norm_rope_kernel<64><<<unsigned(grid), 32 * kRopeWarps, 0, st>>>(p);
-  return launch_status(cudaGetLastError(), "qsa_qk_norm_rope");
+  const auto kernel = D == 256   ? qsa_norm_rope_kernel<256>
+                      : D == 128 ? qsa_norm_rope_kernel<128>
+                                 : qsa_norm_rope_kernel<64>;
+  return launch_status(launch(kernel, unsigned(grid), 32 * kRopeWarps, 0, st, p), "qsa_qk_norm_rope");
 }
 
 extern "C" qsa_status_t qsa_pack_index_keys(const void* keys, int64_t key_stride_s,
@@ -438,7 +440,6 @@ extern "C" qsa_status_t qsa_pack_index_keys(const void* keys, int64_t key_stride
   const int per = kPackThreads / (Di / 8);
   const int grid = int((int64_t(n) + per - 1) / per);
   const auto st = static_cast<cudaStream_t>(stream);
-  if (Di == 128) qsa_pack_index_kernel<128><<<grid, kPackThreads, 0, st>>>(p);
-  else qsa_pack_index_kernel<64><<<grid, kPackThreads, 0, st>>>(p);
-  return launch_status(cudaGetLastError(), "qsa_pack_index_keys");
+  const auto kernel = Di == 128 ? qsa_pack_index_kernel<128> : qsa_pack_index_kernel<64>;
+  return launch_status(launch(kernel, grid, kPackThreads, 0, st, p), "qsa_pack_index_keys");
 }

@@ -31,6 +31,7 @@ struct SelectParams {
   int32_t Tq, B, P, page_size, per_page, Hi, block, top, sink, local;
   int4* tiles;         // tcgen05 form: tiles of rows [chunks, max_tiles], and their codes and gains
   uint8_t* tile_q;
+  int32_t first;       // the choice is the call's first kernel
   int32_t cap, queue, window;              // keys of a row, and words of its marks, in the choice's shared memory
   uint32_t page_magic, block_magic; // 2^32 / per_page (/ block), rounded up
 };
@@ -128,6 +129,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks)
   float* sGain = reinterpret_cast<float*>(smem + size_t(groups) * NT * C::kSteps * 256);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g8 = lane >> 2, u = lane & 3;
+  begin_kernel();
 
   // units of sequence b's rows in this chunk: as many as if every tile saw all of its blocks
   auto rows_here = [&](int b) {
@@ -392,6 +394,7 @@ template <int DI, int HP>
 __global__ void __launch_bounds__(256) qsa_select_prep_kernel(const SelectParams p, int chunk_rows) {
   constexpr int kLanes = DI / 8, kVec = 32 / kLanes;
   __shared__ int sTmp[8], sFound[4];
+  begin_kernel();
   const int c0 = int(min(int64_t(blockIdx.y) * chunk_rows, int64_t(p.Tq)));
   const int c1 = int(min(int64_t(c0) + chunk_rows, int64_t(p.Tq)));
   const int tile = blockIdx.x / kPrepParts, part = blockIdx.x % kPrepParts;
@@ -490,6 +493,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   constexpr int kFull = 0, kFree = kWideStages, kQFull = 2 * kWideStages, kQFree = kQFull + kWideQ,
                 kAccFull = kQFree + kWideQ, kAccFree = kAccFull + 2;
 
+  begin_kernel();
   // ---- this block's share ------------------------------------------------------------------
   int64_t total_units = 0;
   for (int i0 = 0; i0 < max_tiles; i0 += kWideThreads) {
@@ -960,7 +964,12 @@ __global__ void __launch_bounds__(32 * kPickWarps) qsa_select_pick_kernel(const 
   extern __shared__ __align__(16) uint32_t dyn[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row_at = blockIdx.x * kPickWarps + warp, t = p.c0 + row_at;
-  if (t >= p.c1) return;
+  launch_next();
+  if (p.first) wait_for_last();  // (no score kernel came before)
+  if (t >= p.c1) {
+    wait_for_last();
+    return;
+  }
   __shared__ __align__(16) ChooseShared sSearch[kPickWarps];
   uint32_t* sKey = dyn + warp * (p.cap + (p.top + 3) / 4 * 4);
   int* sList = reinterpret_cast<int*>(sKey + p.cap);
@@ -978,9 +987,13 @@ __global__ void __launch_bounds__(32 * kPickWarps) qsa_select_pick_kernel(const 
       if (m != 0u) b = i0 + 31 - __clz(m);  // (offsets that overlap: the last one)
     }
   }
-  if (b < 0) return;
+  if (b < 0) {
+    wait_for_last();
+    return;
+  }
   const int last = rows_of(p, b, false).y - 1, len = length_of(p, b, lane == 0);
   const int seen = max(len - (last - t), 0), f = seen / p.block, taken = min(f, p.top);
+  wait_for_last();  // the scores
   const SlotMap map{p, p.table + b * p.table_st};
   if (f <= p.top) {
     for (int j = lane; j < f; j += 32) sList[j] = map.first_slot(j);
@@ -1076,6 +1089,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : THREADS == 256 
   __shared__ int sTmp[THREADS / 32], sSeq;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t = p.c0 + blockIdx.x;
+  launch_next();
+  if (p.first) wait_for_last();  // (no score kernel came before)
   if (tid == 0) sSeq = (p.cu == nullptr && t < p.B) ? t : -1;
   __syncthreads();
   if (p.cu != nullptr) {
@@ -1086,10 +1101,14 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : THREADS == 256 
     __syncthreads();
   }
   const int b = sSeq;
-  if (b < 0) return;
+  if (b < 0) {
+    wait_for_last();
+    return;
+  }
   const int last = rows_of(p, b, false).y - 1, len = length_of(p, b, tid == 0);
   const int seen = max(len - (last - t), 0);
   const int f = seen / p.block, taken = min(f, p.top);
+  wait_for_last();  // the scores
   const float* row = p.scores + blockIdx.x * p.ld;
   const SlotMap map{p, p.table + b * p.table_st};
   if (f <= p.top) {
@@ -1305,8 +1324,8 @@ cudaError_t launch_score(SelectParams& p, int groups, int num_sms, cudaStream_t 
   const int rows = p.c1 - p.c0;
   const int64_t row_tiles = p.cu == nullptr ? rows : rows / C::kRows + (p.B < rows ? p.B : rows);
   const int64_t most = row_tiles * ((p.ld + kKeyTile - 1) / kKeyTile), all = int64_t(num_sms) * kScoreBlocks;
-  qsa_select_score_kernel<DI, HP, NT><<<unsigned(most < all ? most : all), kScoreThreads, smem, st>>>(p, groups);
-  return cudaGetLastError();
+  return launch(qsa_select_score_kernel<DI, HP, NT>, unsigned(most < all ? most : all), kScoreThreads, smem, st, p,
+                groups);
 }
 
 int heads_padded(int Hi) {
@@ -1328,8 +1347,7 @@ int64_t wide_max_tiles(int32_t rows, int32_t B, int32_t Hi) {  // a sequence add
 template <int DI, int HP>
 cudaError_t launch_prep(const SelectParams& p, int chunk_rows, int chunks, cudaStream_t st) {
   const dim3 grid(unsigned(wide_max_tiles(chunk_rows, p.B, p.Hi) * kPrepParts), unsigned(chunks));
-  qsa_select_prep_kernel<DI, HP><<<grid, 256, 0, st>>>(p, chunk_rows);
-  return cudaGetLastError();
+  return launch(qsa_select_prep_kernel<DI, HP>, grid, 256, 0, st, p, chunk_rows);
 }
 
 template <int DI, int HP>
@@ -1338,9 +1356,9 @@ cudaError_t launch_wide(const SelectParams& p, int chunk, int chunk_rows, int nu
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, Wide<DI>::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t max_tiles = wide_max_tiles(chunk_rows, p.B, p.Hi);
-  qsa_select_wide_kernel<DI, HP><<<num_sms, kWideThreads, Wide<DI>::kSmem, st>>>(
-      p, p.tiles + chunk * max_tiles, p.tile_q + chunk * max_tiles * wide_tile_bytes(DI), int(max_tiles));
-  return cudaGetLastError();
+  return launch(qsa_select_wide_kernel<DI, HP>, num_sms, kWideThreads, Wide<DI>::kSmem, st, p,
+                static_cast<const int4*>(p.tiles + chunk * max_tiles),
+                static_cast<const uint8_t*>(p.tile_q + chunk * max_tiles * wide_tile_bytes(DI)), int(max_tiles));
 }
 
 // prep: the tiles of all chunks (chunk < 0), or the scores of one chunk
@@ -1379,8 +1397,7 @@ cudaError_t launch_choose_for(const SelectParams& p, size_t smem, cudaStream_t s
   const cudaError_t e = cudaFuncSetAttribute(qsa_select_choose_kernel<THREADS>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
-  qsa_select_choose_kernel<THREADS><<<p.c1 - p.c0, THREADS, smem, st>>>(p);
-  return cudaGetLastError();
+  return launch(qsa_select_choose_kernel<THREADS>, p.c1 - p.c0, THREADS, smem, st, p);
 }
 
 cudaError_t launch_choose(SelectParams& p, int num_sms, cudaStream_t st) {
@@ -1392,8 +1409,7 @@ cudaError_t launch_choose(SelectParams& p, int num_sms, cudaStream_t st) {
     const cudaError_t e = cudaFuncSetAttribute(qsa_select_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                int(smem));
     if (e != cudaSuccess) return e;
-    qsa_select_pick_kernel<<<(rows + kPickWarps - 1) / kPickWarps, 32 * kPickWarps, smem, st>>>(p);
-    return cudaGetLastError();
+    return launch(qsa_select_pick_kernel, (rows + kPickWarps - 1) / kPickWarps, 32 * kPickWarps, smem, st, p);
   }
   // room for what the sample's border lets through: about 1.3 to 2 times `top` for long rows
   const int want = p.top * 5 / 2 > 1536 ? p.top * 5 / 2 : 1536;
@@ -1523,7 +1539,8 @@ extern "C" qsa_status_t qsa_select_slots(
   const auto st = static_cast<cudaStream_t>(stream);
   p.page_magic = uint32_t(((uint64_t(1) << 32) + p.per_page - 1) / p.per_page);
   p.block_magic = uint32_t(((uint64_t(1) << 32) + block - 1) / block);
-  const bool scored = ld > top_blocks;  // (a table of at most top_blocks blocks needs no scores)
+  p.first = ld <= top_blocks;
+  const bool scored = !p.first;  // (a table of at most top_blocks blocks needs no scores)
   auto wide_launch = [&](int chunk) {
     return Di == 128 ? launch_wide_for<128>(p, chunk, rows, lay.chunks, num_sms, st)
                      : launch_wide_for<64>(p, chunk, rows, lay.chunks, num_sms, st);
