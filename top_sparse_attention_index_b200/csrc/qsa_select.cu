@@ -42,11 +42,12 @@ __device__ __forceinline__ float kept_score(float sum, float scale) {
   return fmaxf(__fmaf_rn(sum, scale, 0.f), -__builtin_huge_valf());
 }
 
-// The order of scores as an order of unsigned integers, -infinity at kLeastKey; 0 is left for
-// blocks that take no part.  And back.
+// The order of scores as an order of unsigned integers, -infinity at kLeastKey and nothing (not
+// what a failed score kernel left, either) below it; 0 is left for blocks that take no part.
+// And back.
 constexpr uint32_t kLeastKey = 0x007fffffu;
 __device__ __forceinline__ uint32_t order_key(uint32_t score) {
-  return score ^ (uint32_t(int32_t(score) >> 31) | 0x80000000u);
+  return max(score ^ (uint32_t(int32_t(score) >> 31) | 0x80000000u), kLeastKey);
 }
 __device__ __forceinline__ float key_score(uint32_t key) {
   key = max(key, kLeastKey);
@@ -840,7 +841,7 @@ __device__ __forceinline__ void write_row(const SelectParams& p, const SlotMap& 
 struct alignas(16) ChooseShared {  // (the histogram is read 16 bytes at a time)
   int hist[kBins];
   uint32_t few[32];
-  uint32_t lo, hi;
+  uint32_t hi;
   int n_few, bin, above, count, n;
 };
 
@@ -852,47 +853,51 @@ __device__ __forceinline__ void keep_bit(uint32_t& mask, float x, float low, uin
   asm("{\n  .reg .pred q;\n  setp.ge.f32 q, %1, %2;\n  @q or.b32 %0, %0, %3;\n}\n" : "+r"(mask) : "f"(x), "f"(low), "r"(bit));
 }
 
-// The want-th largest (1 <= want <= n) of the keys key_at(0 .. n - 1), by histograms of the
-// key range that still holds it; the last step ranks at most 32 keys within each warp.
-// Without EXACT: a key at most that one with few keys between them (`key` alone is meant).
 template <int THREADS>
 __device__ __forceinline__ void sync_all() {
   if constexpr (THREADS == 32) __syncwarp(); else __syncthreads();
 }
 
+// The want-th largest (at least 1) of the keys keys_at(0 .. n - 1) of four neighbours each, the
+// zeros among them not counted, by histograms of the key range that still holds it; the
+// last step ranks at most 32 keys within each warp.  Without EXACT: a key at most that one
+// with few keys between them (`key` alone is meant).  (The keys come four at a time because
+// no load moves ahead of an atomic: key by key a warp took 10,000 to 27,000 cycles for 500 to
+// 2,000 keys.)
 template <int THREADS, bool EXACT, class F>
-__device__ Border kth_largest(int n, int want, F key_at, ChooseShared& sh) {
+__device__ Border kth_largest(int n, int want, F keys_at, ChooseShared& sh) {
   const int tid = THREADS == 32 ? threadIdx.x & 31 : threadIdx.x, lane = tid & 31;
   sync_all<THREADS>();  // (sh and the keys)
-  if (tid == 0) sh.lo = 0xffffffffu, sh.hi = 0u, sh.n_few = 0;
+  if (tid == 0) sh.hi = kLeastKey, sh.n_few = 0;
   for (int i = tid; i < kBins; i += THREADS) sh.hist[i] = 0;
-  uint32_t lo = 0xffffffffu, hi = 0u;
+  uint32_t hi = 0u;
 #pragma unroll 4
   for (int i = tid; i < n; i += THREADS) {
-    const uint32_t k = key_at(i);
-    lo = min(lo, k);
-    hi = max(hi, k);
+    const uint4 k = keys_at(i);
+    hi = max(max(max(hi, k.x), k.y), max(k.z, k.w));
   }
-  lo = __reduce_min_sync(0xffffffffu, lo);
   hi = __reduce_max_sync(0xffffffffu, hi);
-  sync_all<THREADS>();
-  if (lane == 0 && lo <= hi) {
-    atomicMin(&sh.lo, lo);
-    atomicMax(&sh.hi, hi);
+  if (THREADS > 32) {
+    sync_all<THREADS>();
+    if (lane == 0) atomicMax(&sh.hi, hi);
+    sync_all<THREADS>();
+    hi = sh.hi;
+  } else {
+    hi = max(hi, kLeastKey);
+    sync_all<THREADS>();
   }
-  sync_all<THREADS>();
-  const uint32_t least = sh.lo;
-  hi = sh.hi;
   // The keys are floats in order: most of a row's lie in a few octaves below the largest, so
   // the first histogram takes four of them, and the whole range only if that is not enough.
-  lo = hi - least > (4u << 23) ? hi - (4u << 23) : least;
+  uint32_t lo = hi - kLeastKey > (4u << 23) ? hi - (4u << 23) : kLeastKey;
   for (;;) {
     const uint32_t range = hi - lo;
     const int shift = range < uint32_t(kBins) ? 0 : 32 - __clz(range) - 9;  // 2^9 = kBins
-#pragma unroll 4
-    for (int i = tid; i < n; i += THREADS) {
-      const uint32_t k = key_at(i) - lo;
-      if (k <= range) atomicAdd(&sh.hist[k >> shift], 1);
+    for (int i = tid; i < n; i += 2 * THREADS) {
+      const uint4 a = keys_at(i), b = i + THREADS < n ? keys_at(i + THREADS) : make_uint4(0u, 0u, 0u, 0u);
+      const uint32_t k[8] = {a.x - lo, a.y - lo, a.z - lo, a.w - lo, b.x - lo, b.y - lo, b.z - lo, b.w - lo};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (k[e] <= range) atomicAdd(&sh.hist[k[e] >> shift], 1);
     }
     sync_all<THREADS>();
     if (tid < 32) {  // lane i holds bins 511 - 16 i down to 496 - 16 i
@@ -922,7 +927,8 @@ __device__ Border kth_largest(int n, int want, F key_at, ChooseShared& sh) {
     }
     sync_all<THREADS>();
     if (sh.bin < 0) {  // fewer keys than wanted above lo
-      lo = least;
+      if (lo == kLeastKey) return {lo, want, want};  // (never: at least `want` keys take part)
+      lo = kLeastKey;
       for (int i = tid; i < kBins; i += THREADS) sh.hist[i] = 0;
       sync_all<THREADS>();
       continue;
@@ -934,14 +940,21 @@ __device__ Border kth_largest(int n, int want, F key_at, ChooseShared& sh) {
     if (shift == 0) return {lo, want, count};
     if (count <= 32) {
       if (!EXACT) return {lo, want, count};
-#pragma unroll 4
-      for (int i = tid; i < n; i += THREADS) {
-        const uint32_t k = key_at(i);
-        if (k - lo <= hi - lo) sh.few[atomicAdd(&sh.n_few, 1)] = k;
+      for (int i = tid; i < n; i += 2 * THREADS) {
+        const uint4 a = keys_at(i), b = i + THREADS < n ? keys_at(i + THREADS) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t k[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        bool any = false;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) any |= k[e] - lo <= hi - lo;
+        if (!any) continue;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (k[e] - lo <= hi - lo) sh.few[atomicAdd(&sh.n_few, 1)] = k[e];
       }
       sync_all<THREADS>();
       const uint32_t mine = sh.few[lane < count ? lane : 0];
       int more = 0, same = 0;
+#pragma unroll 4
       for (int i = 0; i < count; ++i) {
         const uint32_t k = __shfl_sync(0xffffffffu, mine, i);
         more += k > mine;
@@ -971,8 +984,8 @@ __global__ void __launch_bounds__(32 * kPickWarps) qsa_select_pick_kernel(const 
     return;
   }
   __shared__ __align__(16) ChooseShared sSearch[kPickWarps];
-  uint32_t* sKey = dyn + warp * (p.cap + (p.top + 3) / 4 * 4);
-  int* sList = reinterpret_cast<int*>(sKey + p.cap);
+  uint32_t* sKey = dyn + warp * p.cap;
+  int* sList = reinterpret_cast<int*>(sKey);  // (a taken block's place is never behind its own key's)
   int b = -1;
   if (p.cu == nullptr) {
     if (t < p.B) b = t;
@@ -1019,7 +1032,7 @@ __global__ void __launch_bounds__(32 * kPickWarps) qsa_select_pick_kernel(const 
     __syncwarp();
     const int want = p.top - p.sink - p.local;
     Border border{0xffffffffu, 0, 0};
-    if (want > 0) border = kth_largest<32, true>(f, want, [&](int i) { return sKey[i]; }, sSearch[warp]);
+    if (want > 0) border = kth_largest<32, true>((f + 3) / 4, want, [&](int i) { return reinterpret_cast<uint4*>(sKey)[i]; }, sSearch[warp]);
     const bool all_same = border.want == border.equal;
     const uint32_t below = (1u << lane) - 1u, least = all_same ? border.key : border.key + 1u;
     int have = 0, same = 0;
@@ -1054,6 +1067,7 @@ __global__ void __launch_bounds__(32 * kPickWarps) qsa_select_pick_kernel(const 
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) at += __popc(take[e] & below);
+      __syncwarp();  // (every lane has its keys of this group)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if ((take[e] >> lane) & 1) sList[at + mine++] = j + e;
@@ -1120,7 +1134,12 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : THREADS == 256 
     auto searched = [&](int j, uint32_t score) { return forced(j) ? 0u : order_key(score); };
     auto in_row = [&](int j) { return searched(j, __float_as_uint(__ldg(row + j))); };
     const uint4* row4 = reinterpret_cast<const uint4*>(row);  // (ld is a multiple of 32)
-    auto in_list = [&](int i) { return sKey[i]; };
+    auto four_in_row = [&](int i) {  // (past the end: not searched)
+      const uint4 k = __ldg(row4 + i);
+      return make_uint4(searched(4 * i, k.x), searched(4 * i + 1, k.y), searched(4 * i + 2, k.z),
+                        searched(4 * i + 3, k.w));
+    };
+    auto four_in_list = [&](int i) { return reinterpret_cast<const uint4*>(sKey)[i]; };
     Border border{0xffffffffu, 0, 0};
     int listed = want > 0 ? -1 : 0;  // keys collected with their blocks; -1: every block of the row is searched
     if (want == 0) {
@@ -1139,7 +1158,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : THREADS == 256 
                                                            searched(j + 2, k[u].z), searched(j + 3, k[u].w));
         }
       }
-      border = kth_largest<THREADS, true>(f, want, in_list, sh);
+      border = kth_largest<THREADS, true>((f + 3) / 4, want, four_in_list, sh);
     } else {
       {
         uint32_t k[kSample / THREADS];  // one from each of kSample equal parts of the row
@@ -1154,7 +1173,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : THREADS == 256 
       // of the row's `want` best, about `hits` are in the sample: the border lies 4 deviations lower
       const float hits = float(want) * kSample / float(f);
       int rank = min(int(hits + 4.f * sqrtf(hits)) + 4, kSample);
-      uint32_t low = kth_largest<THREADS, false>(kSample, rank, in_list, sh).key;
+      uint32_t low = kth_largest<THREADS, false>(kSample / 4, rank, four_in_list, sh).key;
       // The blocks of keys from `low` up: every lane queues the ones it meets (16-bit numbers, in
       // the keys' room), a scan over the lanes then puts the queues together.  More than there
       // is room for: the want-th largest of those that had room is a better border, since as
@@ -1226,12 +1245,13 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : THREADS == 256 
         if (room < want) break;
 #pragma unroll 4
         for (int i = tid; i < room; i += THREADS) sKey[i] = order_key(__float_as_uint(__ldg(row + sIdx[i])));
-        border = kth_largest<THREADS, true>(room, want, in_list, sh);
+        if (tid < 4 && room + tid < (room + 3) / 4 * 4) sKey[room + tid] = 0u;
+        border = kth_largest<THREADS, true>((room + 3) / 4, want, four_in_list, sh);
         if (n == room) listed = n;
         if (n == room || border.key <= low) break;
         low = border.key;
       }
-      if (listed < 0) border = kth_largest<THREADS, true>(f, want, in_row, sh);
+      if (listed < 0) border = kth_largest<THREADS, true>((f + 3) / 4, want, four_in_row, sh);
     }
     // ---- marks and places, a window of blocks at a time ----------------------------------------
     const bool all_same = border.want == border.equal;  // no choice between equal keys
@@ -1405,7 +1425,7 @@ cudaError_t launch_choose(SelectParams& p, int num_sms, cudaStream_t st) {
   // (with few rows the four warps of a block each would leave most of the device idle)
   if (p.ld <= kPickKeys && p.top <= kPickKeys && rows > 2 * num_sms) {
     p.cap = int((p.ld + 127) / 128 * 128);
-    const size_t smem = size_t(kPickWarps) * (p.cap + (p.top + 3) / 4 * 4) * 4;
+    const size_t smem = size_t(kPickWarps) * p.cap * 4;
     const cudaError_t e = cudaFuncSetAttribute(qsa_select_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                int(smem));
     if (e != cudaSuccess) return e;
