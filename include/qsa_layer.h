@@ -15,7 +15,9 @@
  * or synchronised, errors are returned before any launch and leave the outputs untouched,
  * values that the host cannot see are checked on the device and reported through
  * *err_word (QSA_ERRBIT_*, may be NULL).  Sizes of zero are no-ops that return QSA_OK.
- * Results are deterministic: the same inputs give bitwise the same outputs.
+ * Results are deterministic: the same inputs give bitwise the same outputs.  Outputs and the
+ * workspace must not overlap the inputs, except where an argument says so; a workspace is
+ * in use until the call's work on the stream is done.
  */
 #ifndef QSA_LAYER_H_
 #define QSA_LAYER_H_
@@ -62,7 +64,7 @@ extern "C" {
  *                 bf16, or with kv_fp8 E4M3 codes of x * (1 / k_scale) (x * (1 / v_scale)),
  *                 saturated (strides in bytes).  slots[t] = -1 stores nothing; another value outside
  *                 [0, rows) stores nothing and sets QSA_ERRBIT_SLOT_RANGE.  When two tokens
- *                 name one slot, which of them it holds is unspecified.
+ *                 name one slot, what it holds is unspecified.
  *   D is 64, 128 or 256; rot is a multiple of 16, at most D (0: no rotation).
  * Pointers are 16-byte aligned (positions, inv_freq, slots: 4) and strides multiples of 16
  * bytes (8 bytes for E4M3 destinations).

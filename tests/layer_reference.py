@@ -84,6 +84,8 @@ def select(q, weight, codes, scales, table, lens, cu, top, page, block, sink, lo
     B, P = table.shape
     cu = np.arange(B + 1) if cu is None else cu.cpu().numpy()
     per, pages = page // block, codes.shape[0] // (page // block)
+    if pages == 0:  # an empty pool: every page lies outside it
+        codes, scales = np.zeros((1, codes.shape[1]), np.int64), np.zeros(1, np.float32)
     W = top * block + block - 1
     out, width = np.full((Tq, W), -7, np.int32), np.full(Tq, -7, np.int32)
     qc, qs = codes_of(q)

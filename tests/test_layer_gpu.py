@@ -730,3 +730,62 @@ def test_calls_that_read_what_the_call_before_wrote():
     out = qsa.paged_decode(**d)
     want, tol, _ = ref.paged_decode(d["q"], d["k_cache"], d["v_cache"], d["page_table"], base, 64, 1 / 16)
     close(out, want, tol)
+
+
+def test_select_largest_budget_of_many_rows():
+    """8,192 blocks of rows in thread blocks of every size."""
+    x = torch.rand(30000, generator=gen(96), device="cuda") + 0.5
+    for rows in (2, 160, 310):
+        c = keyed_case(x, rows, 0)
+        got, width = run_select(c, 8192, 1, 50)
+        for t in (0, rows - 1):
+            want, want_width = ref.select(c["q"][t:t + 1], c["weight"][t:t + 1], c["codes"], c["scales"], c["page_table"],
+                                          c["seq_lens"] - (rows - 1 - t), None, 8192, c["page_size"], 1, 1, 50)
+            assert torch.equal(got[t].cpu(), torch.from_numpy(want[0])) and int(width[t]) == int(want_width[0])
+
+
+def test_empty_page_tables_and_pools():
+    c = select_case(97, [10, 20], None, 4, 128, 4, 16)
+    empty = dict(c, page_table=c["page_table"][:, :0])
+    assert check_select(empty, 8) == WIDTH_RANGE
+    none = dict(c, codes=c["codes"][:0], scales=c["scales"][:0])
+    assert check_select(none, 8) == SLOT_RANGE and check_select(none, 1) == SLOT_RANGE
+    d = decode_case(98, [10, 20], 8, 1, 16)
+    assert check_decode(dict(d, page_table=d["page_table"][:, :0]))[0] == WIDTH_RANGE
+    assert check_decode(dict(d, k_cache=d["k_cache"][:0], v_cache=d["v_cache"][:0]))[0] == SLOT_RANGE
+
+
+def test_strides_of_dimensions_of_one():
+    """A single token, head or sequence may have any stride in that dimension."""
+    c = decode_case(99, [300], 8, 1, 16)
+    want = qsa.paged_decode(**c)
+    odd = lambda t, d, n: t.as_strided(t.shape, [n if i == d else s for i, s in enumerate(t.stride())])  # noqa: E731
+    got = qsa.paged_decode(**dict(c, q=odd(c["q"], 0, 3), k_cache=odd(c["k_cache"], 1, 5), v_cache=odd(c["v_cache"], 1, 1)))
+    assert torch.equal(got, want)
+    r = rope_case(99, 1, 1, 1, 128, 64, 1)
+    want, _ = qsa.qk_norm_rope(r["q"], r["positions"], r["inv_freq"])
+    got, _ = qsa.qk_norm_rope(odd(odd(r["q"], 0, 1), 1, 7), r["positions"], r["inv_freq"])
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_two_calls_at_once(fp8):
+    """The same inputs on two streams at the same time, each with its own outputs and workspace."""
+    d = decode_case(100, [9000, 40, 3000], 16, 2, 64, fp8)
+    c = select_case(101, [9000, 3000], [300, 200], 4, 128, 4, 64)
+    want = qsa.paged_decode(**d), run_select(c, 100)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for _ in range(3):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append((qsa.paged_decode(**d), run_select(c, 100)))
+    torch.cuda.synchronize()
+    for out, (idx, width) in got:
+        assert torch.equal(out, want[0]) and torch.equal(idx, want[1][0]) and torch.equal(width, want[1][1])
+
+
+def test_stream_of_the_tensors():
+    d = decode_case(102, [30], 8, 1, 16)
+    assert torch.equal(qsa.paged_decode(**d, stream=torch.cuda.current_stream()), qsa.paged_decode(**d))

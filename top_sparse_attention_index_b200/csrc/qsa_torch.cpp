@@ -118,6 +118,10 @@ uint32_t* err_ptr(PyObject* o, at::Device device) {
   return static_cast<uint32_t*>(t->data_ptr());
 }
 
+// The stride of a dimension, 0 where it is never taken (a tensor's views may give it any value).
+int64_t pitch(const Tensor& t, int d) { return t.size(d) > 1 ? t.stride(d) : 0; }
+int64_t pitch(const Tensor* t, int d) { return t == nullptr ? 0 : pitch(*t, d); }
+
 void* ptr(const Tensor* t) { return t == nullptr ? nullptr : t->data_ptr(); }
 const int32_t* ptr32(const Tensor* t) { return static_cast<const int32_t*>(ptr(t)); }
 
@@ -225,14 +229,13 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Tensor k_out;
     if (k != nullptr && k_cache == nullptr) k_out = empty({T, Hkv, D}, kBF16, device);
     const Tensor* k_dst = k_cache != nullptr ? k_cache : k != nullptr ? &k_out : nullptr;
-    const auto st_of = [](const Tensor* t, int d) { return t == nullptr ? int64_t(0) : t->stride(d); };
     const qsa_status_t st = qsa_qk_norm_rope(
-        q.data_ptr(), q.stride(0), q.stride(1), ptr(k), st_of(k, 0), st_of(k, 1), ptr(v), st_of(v, 0), st_of(v, 1),
-        ptr(qw), ptr(kw), offset, eps, ptr32(&pos), axes > 1 ? pos.stride(0) : 0,
+        q.data_ptr(), pitch(q, 0), pitch(q, 1), ptr(k), pitch(k, 0), pitch(k, 1), ptr(v), pitch(v, 0), pitch(v, 1),
+        ptr(qw), ptr(kw), offset, eps, ptr32(&pos), axes > 1 ? pitch(pos, 0) : 0,
         static_cast<const float*>(inv_freq.data_ptr()), size32("inv_freq", rot), interleaved,
         has_sections ? sections : nullptr, size32("positions", axes), rope_scale, size32("T", T), size32("Hq", Hq),
-        size32("Hkv", Hkv), size32("D", D), q_out.data_ptr(), q_out.stride(0), q_out.stride(1), ptr(k_dst),
-        st_of(k_dst, 0), st_of(k_dst, 1), ptr(v_cache), st_of(v_cache, 0), st_of(v_cache, 1), ptr32(slots), rows,
+        size32("Hkv", Hkv), size32("D", D), q_out.data_ptr(), pitch(q_out, 0), pitch(q_out, 1), ptr(k_dst),
+        pitch(k_dst, 0), pitch(k_dst, 1), ptr(v_cache), pitch(v_cache, 0), pitch(v_cache, 1), ptr32(slots), rows,
         fp8 ? 1 : 0, ks, vs, err, stream_of(device));
     if (st != QSA_OK) return status(st);
     PyObject* r = PyTuple_New(2);
@@ -268,9 +271,9 @@ PyObject* pack_index_keys(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check("scales", scales, kF32, device, {S / block});
     uint32_t* err = err_ptr(a[5], device);
     const c10::cuda::OptionalCUDAGuard guard(device);
-    return status(qsa_pack_index_keys(keys.data_ptr(), keys.stride(0), ptr32(&blocks), size32("blocks", blocks.size(0)),
+    return status(qsa_pack_index_keys(keys.data_ptr(), pitch(keys, 0), ptr32(&blocks), size32("blocks", blocks.size(0)),
                                       block, size32("Di", Di), S, static_cast<int8_t*>(codes.data_ptr()),
-                                      codes.stride(0), static_cast<float*>(scales.data_ptr()), err, stream_of(device)));
+                                      pitch(codes, 0), static_cast<float*>(scales.data_ptr()), err, stream_of(device)));
   });
 }
 
@@ -314,10 +317,10 @@ PyObject* select_slots(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor width = given_width != nullptr ? *given_width : empty({Tq}, kI32, device);
     const Tensor work = given_work != nullptr ? *given_work : empty({int64_t(need)}, kU8, device);
     const qsa_status_t st = qsa_select_slots(
-        q.data_ptr(), q.stride(0), q.stride(1), static_cast<const float*>(weight.data_ptr()), weight.stride(0),
-        static_cast<const int8_t*>(codes.data_ptr()), codes.stride(0), static_cast<const float*>(scales.data_ptr()),
-        ptr32(&table), table.stride(0), ptr32(&lens), ptr32(cu), tq, b, p, codes.size(0) / (page / block), page, hi, di,
-        block, top, sink, local, static_cast<int32_t*>(idx.data_ptr()), idx.stride(0),
+        q.data_ptr(), pitch(q, 0), pitch(q, 1), static_cast<const float*>(weight.data_ptr()), pitch(weight, 0),
+        static_cast<const int8_t*>(codes.data_ptr()), pitch(codes, 0), static_cast<const float*>(scales.data_ptr()),
+        ptr32(&table), pitch(table, 0), ptr32(&lens), ptr32(cu), tq, b, p, codes.size(0) / (page / block), page, hi, di,
+        block, top, sink, local, static_cast<int32_t*>(idx.data_ptr()), pitch(idx, 0),
         static_cast<int32_t*>(width.data_ptr()), work.data_ptr(), size_t(work.numel()), err, stream_of(device));
     if (st != QSA_OK) return status(st);
     PyObject* r = PyTuple_New(2);
@@ -374,9 +377,9 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor out = given != nullptr ? *given : empty({B, Hq, D}, kBF16, device);
     const Tensor work = given_work != nullptr ? *given_work : need > 0 ? empty({int64_t(need)}, kU8, device) : Tensor();
     const qsa_status_t st = qsa_paged_decode(
-        q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
-        v.stride(1), ptr32(&table), table.stride(0), ptr32(&lens), b, hq, hkv, d, p, S / page, page, scale, fp8 ? 1 : 0,
-        ks, vs, out.data_ptr(), out.stride(0), out.stride(1), static_cast<float*>(ptr(lse)), blocks,
+        q.data_ptr(), pitch(q, 0), pitch(q, 1), k.data_ptr(), pitch(k, 0), pitch(k, 1), v.data_ptr(), pitch(v, 0),
+        pitch(v, 1), ptr32(&table), pitch(table, 0), ptr32(&lens), b, hq, hkv, d, p, S / page, page, scale, fp8 ? 1 : 0,
+        ks, vs, out.data_ptr(), pitch(out, 0), pitch(out, 1), static_cast<float*>(ptr(lse)), blocks,
         work.defined() ? work.data_ptr() : nullptr, work.defined() ? size_t(work.numel()) : 0, err, stream_of(device));
     if (st != QSA_OK) return status(st);
     if (given != nullptr) {
