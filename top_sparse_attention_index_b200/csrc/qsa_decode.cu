@@ -103,8 +103,8 @@ struct Decode {
 };
 
 // The units of all sequences are shared out evenly over the thread blocks that the device
-// holds at once, whatever the lengths (split evenly by the page table's capacity, 64 ragged
-// sequences took 157 us, so 113); a sequence that one block holds whole is written to the
+// holds at once, whatever the lengths (64 ragged sequences: 111 us; split evenly by the page
+// table's capacity, 157); a sequence that one block holds whole is written to the
 // output, a piece of one to the block's record (its first piece to record 0, its last to
 // record 1: pieces between them are whole sequences).
 // Within a block each warp takes its 16-slot sub-tiles of a unit and runs a pipeline of its
@@ -113,6 +113,8 @@ struct Decode {
 // shares every row that is read; the softmax is online (base 2, the reference moves only when
 // the maximum rises by more than 2^8); P is rounded to 16 bits for O^T += V^T P^T, and the
 // denominator sums the same rounded values.  The bound is HBM: every row is read once.
+// 64 sequences of up to 8,192 tokens, 24 + 2 heads: 605 MB in 111 us, 0.84 of the copy rate
+// (and 8 us for the join); 4 of 262,144 tokens in E4M3: 1.07 GB in 182 us, 0.91.
 template <bool FP8, int NT>
 __global__ void __launch_bounds__(Decode<FP8, NT>::kThreads) qsa_paged_decode_kernel(const DecodeParams p) {
   using C = Decode<FP8, NT>;
@@ -175,7 +177,7 @@ __global__ void __launch_bounds__(Decode<FP8, NT>::kThreads) qsa_paged_decode_ke
   // The sub-tile's rows, 16 bytes per lane and copy: a row is kRow / 16 lanes.  Lane r looks up
   // slot r; rows past the end or in a page outside the pool are not read, and become zeros.
   // (One bulk copy per row, issued by its own lane, cost more instructions than everything
-  // else here: 235 us for 1.07 GB of E4M3 rows.)
+  // else here: 226 us for 1.07 GB of E4M3 rows, 203 with these copies and two warps.)
   constexpr int kRowLanes = C::kRow / 16, kRows = 32 / kRowLanes;  // lanes of a row, rows of a copy
   const uint8_t* kl = kg + (lane % kRowLanes) * 16;
   const uint8_t* vl = vg + (lane % kRowLanes) * 16;

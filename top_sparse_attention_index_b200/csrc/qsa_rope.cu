@@ -63,7 +63,9 @@ __device__ __forceinline__ uint2 pairs_to_e4m3x8(const uint64_t (&x)[4], uint64_
 // vectors l and l + rot / 16 for the rotated part; otherwise neighbours), so the rotation
 // crosses no lanes and a lane's eight (cos, sin) and its weights stay in registers for all
 // its rows; two values per arithmetic instruction; a step loads while the last is worked on.
-// Bound: every byte is read and written once, HBM.
+// Bound: every byte is read and written once, HBM.  16,384 tokens of 24 + 2 + 2 heads (470 MB):
+// 94 us, 0.77 of the copy rate; what is left is issue slots, 20 warps to an SM.  (A vector per
+// lane, shuffles for the pairs and a thread block per token took 149 us.)
 template <int D>
 __global__ void __launch_bounds__(32 * kRopeWarps, 5) qsa_norm_rope_kernel(const RopeParams p) {
   constexpr int kLanes = D / 16;      // lanes of a row
@@ -240,6 +242,8 @@ struct PackParams {
 
 // Di / 8 lanes per micro-block, each summing its eight dimensions over the block's slots
 // in order; the maximum crosses the lanes by shuffles.  HBM-bound: the keys are read once.
+// 65,536 blocks of 4 keys of 128 (76 MB): 20 us, 0.58 of the copy rate; the chain of a
+// block's number, its keys and the maximum is what the rest waits for.
 constexpr int kPackThreads = 128;
 template <int DI>
 __global__ void __launch_bounds__(kPackThreads) qsa_pack_index_kernel(const PackParams p) {

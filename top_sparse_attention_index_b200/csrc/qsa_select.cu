@@ -119,8 +119,8 @@ struct Score {
 // are put in the same order; so the codes go from memory to the MMA without shared memory,
 // the next blocks' loads in flight, and the page lookups one step further ahead.
 // Bound: HBM, the codes are read once per four rows or more of a sequence.
-// (128-block tiles through shared memory with a barrier each, split evenly by the page table's
-// capacity, took 44 us for 64 rows over ragged caches of up to 16,384 blocks.)
+// 64 rows over ragged caches of up to 16,384 blocks (78 MB): 29 us (128-block tiles through
+// shared memory with a barrier each, split evenly by the page table's capacity: 44 us).
 template <int DI, int HP, int NT>
 __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks)
     qsa_select_score_kernel(const SelectParams p, int groups) {
@@ -471,13 +471,19 @@ struct Wide {
   static constexpr int kSmem = kWideStages * kKeyBytes + kWideQ * kQBytes + kWideStages * kKeyTile * 4;
 };
 
+// score(j) = scales[j] sum_h g_h max(0, c_h . codes[j]), the products of codes in 8-bit MMAs.
 // One thread block per SM walks an equal share of all (tile of rows, tile of keys) pairs.
-// Four warps bring key tiles in (16-byte asynchronous copies through the page table, a
-// stage ahead of their page lookups), one thread issues the MMAs into two accumulators, eight
-// warps turn dots into keys.  What bounds it is those warps' integer and float
-// instructions: per pair of dots an add-with-maximum each (the integer to float conversion
-// 2^23 + max(d, 0) and the clamp at once; a dot of 128 codes is below 2^21), and a packed
-// subtraction, product and sum.
+// Two groups of four warps bring key tiles in (16-byte asynchronous copies through the page
+// table, a step behind their page lookups), one thread issues the MMAs into two
+// accumulators, sixteen warps turn dots into scores.  What bounds it is those warps'
+// instructions, not the MMAs (512 cycles of a unit's 3,400): per pair of dots an
+// add-with-maximum each (the integer to float conversion 2^23 + max(d, 0) and the clamp at
+// once; a dot of 128 codes is below 2^21), and a packed subtraction, product and sum.
+// 7,810 rows of 4 heads over 14,400 to 16,384 blocks of 128 codes: 181 us, 0.68 P op/s (the
+// same through warp-level MMAs with 64 columns a thread block took 1,000 us); eight warps
+// with 128 columns each were 7 % slower, and neither the stores, the gains' loads nor the
+// conversion's form (int to float instructions, or the subtraction folded into the product)
+// moves the time.
 template <int DI, int HP>
 __global__ void __launch_bounds__(kWideThreads, 1)
     qsa_select_wide_kernel(const SelectParams p, const int4* tiles, const uint8_t* tile_q, int max_tiles) {
@@ -971,8 +977,9 @@ __device__ Border kth_largest(int n, int want, F keys_at, ChooseShared& sh) {
 }
 
 // Rows of at most kPickKeys blocks, a warp each: its keys lie in the warp's shared memory,
-// nothing is shared between warps, and no barrier is waited for.  Bound: instructions, about
-// two per key and pivot, ten per key to collect the taken ones in order, and the output.
+// nothing is shared between warps, and no barrier is waited for.  Bound: the latency of its
+// steps in shared memory, with 20 warps to an SM.  16,384 rows of up to 2,048 blocks, 512
+// taken: 110 us.
 __global__ void __launch_bounds__(32 * kPickWarps) qsa_select_pick_kernel(const SelectParams p) {
   extern __shared__ __align__(16) uint32_t dyn[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1087,9 +1094,9 @@ __global__ void __launch_bounds__(32 * kPickWarps) qsa_select_pick_kernel(const 
 // and for keys that repeat with the sample's period: such a row searches its keys in place).
 // The exact border follows from what was collected; a bit per block marks the taken ones,
 // and a scan over the marks gives them their places in ascending order.
-// Bound: the instructions over a row's keys and its output, with the keys read from L2 once
-// (radix passes over the whole row, four reads and a conflicting shared-memory atomic per key
-// and pass, took 165 us per 1,024 rows of 15,500 blocks).
+// Bound: instructions and the latency of its steps, 10 rows to an SM; the scores are read
+// once.  7,810 rows of 15,400 blocks, 512 taken: 244 us (radix passes over the whole row, four
+// reads and a conflicting shared-memory atomic per score and pass, took 1,250).
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : THREADS == 256 ? 4 : 1) qsa_select_choose_kernel(const SelectParams p) {
   constexpr int kBatch = THREADS == 1024 ? 4 : 2;  // 16-byte loads of keys per thread and step
@@ -1177,11 +1184,13 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : THREADS == 256 
       // The blocks of keys from `low` up: every lane queues the ones it meets (16-bit numbers, in
       // the keys' room), a scan over the lanes then puts the queues together.  More than there
       // is room for: the want-th largest of those that had room is a better border, since as
-      // many keys as wanted reach it.  Fewer than wanted, or no better border: every block of
-      // the row is searched.
+      // many keys as wanted reach it (if it is the border they were collected by, the keys above it
+      // come next).  Otherwise every block of the row is searched.
       uint16_t* queue = reinterpret_cast<uint16_t*>(sKey);
       const int longest = p.queue / THREADS;
       constexpr int kStep = THREADS * kBatch;  // 16-byte loads of a step
+      int tied = 0;  // keys from low - 1 up, when the want-th largest of some of them is low - 1
+      bool found = false;
       for (int tries = 0; tries < 3; ++tries) {
         __syncthreads();
         if (tid == 0) sh.n = 0;
@@ -1242,16 +1251,23 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : THREADS == 256 
         if (lane == 0) atomicAdd(&sh.n, all);
         __syncthreads();
         const int n = sh.n, room = min(have, p.cap);
-        if (room < want) break;
+        if (room < want) {
+          // above a key that more share than there is room for: that one is the border
+          if (tied > 0 && n < want) border = {low - 1u, want - n, tied - n}, found = true;
+          break;
+        }
 #pragma unroll 4
         for (int i = tid; i < room; i += THREADS) sKey[i] = order_key(__float_as_uint(__ldg(row + sIdx[i])));
         if (tid < 4 && room + tid < (room + 3) / 4 * 4) sKey[room + tid] = 0u;
         border = kth_largest<THREADS, true>((room + 3) / 4, want, four_in_list, sh);
-        if (n == room) listed = n;
-        if (n == room || border.key <= low) break;
-        low = border.key;
+        if (n == room) {
+          listed = n;
+          break;
+        }
+        tied = border.key <= low ? n : 0;
+        low = tied > 0 ? low + 1u : border.key;
       }
-      if (listed < 0) border = kth_largest<THREADS, true>((f + 3) / 4, want, four_in_row, sh);
+      if (listed < 0 && !found) border = kth_largest<THREADS, true>((f + 3) / 4, want, four_in_row, sh);
     }
     // ---- marks and places, a window of blocks at a time ----------------------------------------
     const bool all_same = border.want == border.equal;  // no choice between equal keys
@@ -1274,12 +1290,20 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : THREADS == 256 
         }
       } else {
         __syncthreads();
-        for (int w = warp; w < words; w += THREADS / 32) {
-          const int j = (w0 + w) * 32 + lane;
-          const uint32_t k = j < f ? (f <= p.cap ? sKey[j] : in_row(j)) : 0u;
-          const uint32_t o = __ballot_sync(0xffffffffu, j < f && (over(k) || forced(j)));
-          const uint32_t s = __ballot_sync(0xffffffffu, j < f && !all_same && k == border.key && !forced(j));
-          if (lane == 0) sOver[w] = o, sSame[w] = s;
+        for (int w = warp * 4; w < words; w += THREADS / 8) {  // four words of a warp at once
+          uint32_t k[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int j = (w0 + w + u) * 32 + lane;
+            k[u] = w + u < words && j < f ? (f <= p.cap ? sKey[j] : in_row(j)) : 0u;
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int j = (w0 + w + u) * 32 + lane;
+            const uint32_t o = __ballot_sync(0xffffffffu, j < f && (over(k[u]) || forced(j)));
+            const uint32_t s = __ballot_sync(0xffffffffu, j < f && !all_same && k[u] == border.key && !forced(j));
+            if (lane == 0 && w + u < words) sOver[w + u] = o, sSame[w + u] = s;
+          }
         }
       }
       __syncthreads();
@@ -1355,9 +1379,11 @@ int heads_padded(int Hi) {
 }
 
 // The tcgen05 form (a pair of rows within 64 columns: at most 32 heads) pays once a tile's 256
-// columns are filled to a quarter on average.
+// columns are filled to more than a half on average.  16 sequences of 16,384 tokens, whole
+// calls, the few-rows form against this one: 4 heads, 16 rows each 35 against 40 us, 32 rows
+// 48 / 51, 64 rows 62 / 51, 128 rows 101 / 70; 16 heads, 8 rows 33 / 38, 16 rows 39 / 36.
 bool use_wide(int32_t Tq, int32_t B, int32_t Hi, bool has_cu) {
-  return has_cu && Hi <= 32 && int64_t(Tq) * heads_padded(Hi) * 4 >= int64_t(B) * kWideCols;
+  return has_cu && Hi <= 32 && int64_t(Tq) * heads_padded(Hi) * 2 > int64_t(B) * kWideCols;
 }
 
 int64_t wide_max_tiles(int32_t rows, int32_t B, int32_t Hi) {  // a sequence adds at most one partial tile
@@ -1410,8 +1436,6 @@ cudaError_t launch_score_for(SelectParams& p, int num_sms, cudaStream_t st) {
   return launch_score<DI, 1, 1>(p, 1, num_sms, st);
 }
 
-// Many rows: small thread blocks, of which an SM holds many.  A row or a few per SM (a decode
-// step): the largest ones, since the row's own latency is the time.
 template <int THREADS>
 cudaError_t launch_choose_for(const SelectParams& p, size_t smem, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(qsa_select_choose_kernel<THREADS>,
@@ -1422,8 +1446,9 @@ cudaError_t launch_choose_for(const SelectParams& p, size_t smem, cudaStream_t s
 
 cudaError_t launch_choose(SelectParams& p, int num_sms, cudaStream_t st) {
   const int rows = p.c1 - p.c0;
-  // (with few rows the four warps of a block each would leave most of the device idle)
-  if (p.ld <= kPickKeys && p.top <= kPickKeys && rows > 2 * num_sms) {
+  // Short rows, a warp each, once there are enough of them: 600 rows of 2,048 blocks take 46 us
+  // so and 41 by a block of 256 per row, 1,200 rows 47 and 47, 2,400 rows 54 and 64 (whole calls).
+  if (p.ld <= kPickKeys && p.top <= kPickKeys && rows > 8 * num_sms) {
     p.cap = int((p.ld + 127) / 128 * 128);
     const size_t smem = size_t(kPickWarps) * p.cap * 4;
     const cudaError_t e = cudaFuncSetAttribute(qsa_select_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1431,19 +1456,27 @@ cudaError_t launch_choose(SelectParams& p, int num_sms, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     return launch(qsa_select_pick_kernel, (rows + kPickWarps - 1) / kPickWarps, 32 * kPickWarps, smem, st, p);
   }
-  // room for what the sample's border lets through: about 1.3 to 2 times `top` for long rows
-  const int want = p.top * 5 / 2 > 1536 ? p.top * 5 / 2 : 1536;
+  // Room for what the sample's border lets through of the longest row: the expected number and
+  // five deviations (a row that does not fit is collected twice), within what a block can
+  // have.
+  const double share = double(p.ld) / kSample, hits = p.top / share;
+  const double rank = hits + 4 * std::sqrt(hits) + 4, room = share * (rank + 5 * std::sqrt(rank));
+  int want = p.top * 5 / 2 > 1536 ? p.top * 5 / 2 : 1536;
+  want = room > want ? (room < 16384 ? int(room) : (want > 16384 ? want : 16384)) : want;
   p.cap = int(p.ld < want ? (p.ld < kSample ? kSample : p.ld) : want);
   p.cap = (p.cap + 127) / 128 * 128;
   p.window = p.ld / 32 < kWindow ? int(p.ld / 32) : kWindow;  // (ld is a multiple of 32)
-  const int threads = rows > 2 * num_sms ? 128 : rows > num_sms ? 256 : 1024;
+  // Threads of a row: one row of 65,535 blocks takes 29 us with 1,024 and 73 with 256; 200 rows of
+  // 8,192 blocks 87 and 76; 600 rows 183 with 256 and 191 with 128; 7,810 rows of 16,384 blocks
+  // 490 and 436 (whole calls).
+  const int threads = rows > 8 * num_sms ? 128 : rows > num_sms ? 256 : 1024;
   // a lane's queue: at least 24 entries (about 8 are expected of 128 lanes, fewer of more)
   p.queue = 2 * p.cap > 24 * threads ? 2 * p.cap / (2 * threads) * (2 * threads) : 24 * threads;
   const size_t keys = p.ld > p.cap ? size_t(p.cap > p.queue / 2 ? p.cap : p.queue / 2) + p.cap : size_t(p.cap);
   const size_t smem = keys * 4 + size_t(p.top + 3) / 4 * 16 + size_t(p.window) * 8;
-  return rows > 2 * num_sms ? launch_choose_for<128>(p, smem, st)
-         : rows > num_sms   ? launch_choose_for<256>(p, smem, st)
-                            : launch_choose_for<1024>(p, smem, st);
+  return threads == 128   ? launch_choose_for<128>(p, smem, st)
+         : threads == 256 ? launch_choose_for<256>(p, smem, st)
+                          : launch_choose_for<1024>(p, smem, st);
 }
 
 // The workspace: keys of a chunk of rows, then the tiles of all chunks.  Sized for the call
