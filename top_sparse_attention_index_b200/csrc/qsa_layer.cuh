@@ -80,11 +80,6 @@ __device__ __forceinline__ void bf16x8_to_f32(const uint4& r, float (&x)[8]) {
   }
 }
 
-__device__ __forceinline__ uint4 f32_to_bf16x8(const float (&x)[8]) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                    pack_bf16x2(x[6], x[7]));
-}
-
 // Two floats -> two E4M3 codes (round to nearest even, saturated); `lo` in the low byte.
 __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
   uint16_t r;
@@ -165,21 +160,6 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity) {
     if (poll_phase(bar, parity)) return true;
   } while (clock_ns() - start < 1000000000u);
   return false;
-}
-
-// The same without suspending the thread: for waits on a pipeline's critical path.
-__device__ __forceinline__ bool spin_phase(uint32_t bar, uint32_t parity) {
-  for (uint32_t n = 0;; ++n) {
-    uint32_t done;
-    asm volatile(
-        "{\n  .reg .pred p;\n  mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        "  selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (done) return true;
-    if (n == 4096) return wait_phase(bar, parity);
-  }
 }
 
 // Bulk copy from this device's memory to shared memory, completing on an mbarrier; both

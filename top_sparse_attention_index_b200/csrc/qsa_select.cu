@@ -488,7 +488,7 @@ template <int DI, int HP>
 __global__ void __launch_bounds__(kWideThreads, 1)
     qsa_select_wide_kernel(const SelectParams p, const int4* tiles, const uint8_t* tile_q, int max_tiles) {
   using C = Wide<DI>;
-  extern __shared__ __align__(1024) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* sQ = smem + kWideStages * C::kKeyBytes;
   float* sScale = reinterpret_cast<float*>(sQ + kWideQ * C::kQBytes);             // [stages][128]
   // key stage full / free, Q full / free, accumulator full / free
@@ -945,31 +945,34 @@ __device__ Border kth_largest(int n, int want, F keys_at, ChooseShared& sh) {
     hi = lo + min(hi - lo, (1u << shift) - 1u);
     if (shift == 0) return {lo, want, count};
     if (count <= 32) {
-      if (!EXACT) return {lo, want, count};
-      for (int i = tid; i < n; i += 2 * THREADS) {
-        const uint4 a = keys_at(i), b = i + THREADS < n ? keys_at(i + THREADS) : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t k[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        bool any = false;
+      if constexpr (!EXACT) {
+        return {lo, want, count};
+      } else {
+        for (int i = tid; i < n; i += 2 * THREADS) {
+          const uint4 a = keys_at(i), b = i + THREADS < n ? keys_at(i + THREADS) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t k[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+          bool any = false;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) any |= k[e] - lo <= hi - lo;
-        if (!any) continue;
+          for (int e = 0; e < 8; ++e) any |= k[e] - lo <= hi - lo;
+          if (!any) continue;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (k[e] - lo <= hi - lo) sh.few[atomicAdd(&sh.n_few, 1)] = k[e];
-      }
-      sync_all<THREADS>();
-      const uint32_t mine = sh.few[lane < count ? lane : 0];
-      int more = 0, same = 0;
+          for (int e = 0; e < 8; ++e)
+            if (k[e] - lo <= hi - lo) sh.few[atomicAdd(&sh.n_few, 1)] = k[e];
+        }
+        sync_all<THREADS>();
+        const uint32_t mine = sh.few[lane < count ? lane : 0];
+        int more = 0, same = 0;
 #pragma unroll 4
-      for (int i = 0; i < count; ++i) {
-        const uint32_t k = __shfl_sync(0xffffffffu, mine, i);
-        more += k > mine;
-        same += k == mine;
+        for (int i = 0; i < count; ++i) {
+          const uint32_t k = __shfl_sync(0xffffffffu, mine, i);
+          more += k > mine;
+          same += k == mine;
+        }
+        const uint32_t at = __ballot_sync(0xffffffffu, lane < count && more < want && more + same >= want);
+        const int src = __ffs(at) - 1;
+        return {__shfl_sync(0xffffffffu, mine, src), want - __shfl_sync(0xffffffffu, more, src),
+                __shfl_sync(0xffffffffu, same, src)};
       }
-      const uint32_t at = __ballot_sync(0xffffffffu, lane < count && more < want && more + same >= want);
-      const int src = __ffs(at) - 1;
-      return {__shfl_sync(0xffffffffu, mine, src), want - __shfl_sync(0xffffffffu, more, src),
-              __shfl_sync(0xffffffffu, same, src)};
     }
     for (int i = tid; i < kBins; i += THREADS) sh.hist[i] = 0;
     sync_all<THREADS>();
