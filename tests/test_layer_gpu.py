@@ -791,3 +791,10 @@ def test_two_calls_at_once(fp8):
 def test_stream_of_the_tensors():
     d = decode_case(102, [30], 8, 1, 16)
     assert torch.equal(qsa.paged_decode(**d, stream=torch.cuda.current_stream()), qsa.paged_decode(**d))
+
+
+@pytest.mark.parametrize("Hi", [1, 4, 12, 24])
+def test_select_prefill_and_decode_rows_in_one_batch(Hi):
+    """Long tiles of rows beside sequences of a row or a few."""
+    lens, rows = [3000] + [700, 1300, 90, 2001, 5, 900] * 2, [700] + [1, 1, 2, 1, 3, 9] * 2
+    assert check_select(select_case(103, lens, rows, Hi, 128, 4, 64, gap=1), 20, 1, 2) == 0
