@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(Decode<FP8, NT>::kThreads) qsa_paged_decode_ke
         m = __umulhi(uint32_t(i), p.page_magic);  // i / page_size, or one more
         if (int64_t(m) * p.page_size > i) --m;
       }
-      const int page = __ldg(p.table + b * p.table_st + m);
+      const int page = p.table[b * p.table_st + m];
       ok = page >= 0 && page < p.pages;
       if (!ok && p.err_word != nullptr) atomicOr(p.err_word, QSA_ERRBIT_SLOT_RANGE);
       slot = ok ? page * p.page_size + (i - m * p.page_size) : 0;
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(THREADS) qsa_paged_join_kernel(const DecodePar
   const int shift = share.begin(first) < seg0 ? 1 : 0;
   auto record = [&](int i) { return (((int64_t(first) + i) * p.Hkv + j) * 2 + (i == 0 ? shift : 0)) * p.G + g; };
   float top = kNegInf;
-  for (int i = tid; i < n; i += THREADS) top = fmaxf(top, __ldcg(p.ws_lse + record(i)));
+  for (int i = tid; i < n; i += THREADS) top = fmaxf(top, load_l2(p.ws_lse + record(i)));
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
   if (lane == 0) sRed[warp] = top;
@@ -498,8 +498,8 @@ __global__ void __launch_bounds__(THREADS) qsa_paged_join_kernel(const DecodePar
 #pragma unroll 4
   for (int i = part; i < n; i += kParts) {
     const int64_t rec = record(i);
-    const float ls = __ldcg(p.ws_lse + rec);
-    const float4 x = __ldcg(reinterpret_cast<const float4*>(p.ws_o + rec * kD + l * 4));
+    const float ls = load_l2(p.ws_lse + rec);
+    const float4 x = load_l2(reinterpret_cast<const float4*>(p.ws_o + rec * kD + l * 4));
     if (ls == kNegInf) continue;  // a piece without a valid page
     const float f = fast_exp2(ls - top);
     sum += f;

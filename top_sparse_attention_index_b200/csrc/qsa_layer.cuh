@@ -46,6 +46,27 @@ __device__ __forceinline__ void begin_kernel() {
   launch_next();
 }
 
+// What an earlier kernel of the stream wrote is read after that wait, by plain loads, or by
+// these, which pass the L1 by; never by the read-only path (__ldg), which is defined only for
+// memory that nobody writes while the kernel exists, and a kernel launched early exists while
+// the one before it still writes.  The asm is volatile: it stays behind the wait.
+__device__ __forceinline__ float load_l2(const float* p) {
+  float x;
+  asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(x) : "l"(__cvta_generic_to_global(p)));
+  return x;
+}
+__device__ __forceinline__ uint4 load_l2(const uint4* p) {
+  uint4 x;
+  asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "l"(__cvta_generic_to_global(p)));
+  return x;
+}
+__device__ __forceinline__ float4 load_l2(const float4* p) {
+  const uint4 x = load_l2(reinterpret_cast<const uint4*>(p));
+  return make_float4(__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w));
+}
+
 template <class... P, class... A>
 cudaError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg{};

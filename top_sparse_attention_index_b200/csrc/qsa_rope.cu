@@ -166,8 +166,8 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 5) qsa_norm_rope_kernel(const
       w = kind == 0 ? p.qw : kind == 1 ? p.kw : nullptr;
       if (w != nullptr) {
         const uint64_t offset2 = pack2(p.offset, p.offset);
-        bf16x8_to_pairs(__ldg(reinterpret_cast<const uint4*>(w + va * 8)), wa);
-        bf16x8_to_pairs(__ldg(reinterpret_cast<const uint4*>(w + vb * 8)), wb);
+        bf16x8_to_pairs(*reinterpret_cast<const uint4*>(w + va * 8), wa);
+        bf16x8_to_pairs(*reinterpret_cast<const uint4*>(w + vb * 8), wb);
 #pragma unroll
         for (int e = 0; e < 4; ++e) wa[e] = add2(wa[e], offset2), wb[e] = add2(wb[e], offset2);
       }

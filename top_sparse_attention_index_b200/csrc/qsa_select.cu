@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks)
             if (int64_t(m) * p.per_page > j) --m;
           }
           off[h] = j - m * p.per_page;
-          page[h] = __ldg(table + m);
+          page[h] = table[m];
         }
       }
     };
@@ -216,10 +216,10 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks)
 #pragma unroll
         for (int i = 0; i < DI / 64; ++i) next_key[h][i] = make_uint4(0u, 0u, 0u, 0u);
         if (ok) {
-          next_scale[h] = __ldg(p.scales + phys);
+          next_scale[h] = p.scales[phys];
 #pragma unroll
           for (int i = 0; i < DI / 64; ++i)
-            next_key[h][i] = __ldg(reinterpret_cast<const uint4*>(p.codes + phys * p.code_st + i * 64 + u * 16));
+            next_key[h][i] = *reinterpret_cast<const uint4*>(p.codes + phys * p.code_st + i * 64 + u * 16);
         }
       }
     };
@@ -418,8 +418,8 @@ __global__ void __launch_bounds__(256) qsa_select_prep_kernel(const SelectParams
       raw[u] = make_uint4(0u, 0u, 0u, 0u);
       gain[u] = 0.f;
       if (row < w.n && head < p.Hi) {
-        raw[u] = __ldg(reinterpret_cast<const uint4*>(p.q + (w.t0 + row) * p.q_st + head * p.q_sh + l * 8));
-        gain[u] = __ldg(p.weight + (w.t0 + row) * p.w_st + head);
+        raw[u] = *reinterpret_cast<const uint4*>(p.q + (w.t0 + row) * p.q_st + head * p.q_sh + l * 8);
+        gain[u] = p.weight[(w.t0 + row) * p.w_st + head];
       }
     }
 #pragma unroll
@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         if (int64_t(m) * p.per_page > j) --m;
       }
       off = j - m * p.per_page;
-      page = __ldg(p.table + w.x * p.table_st + m);
+      page = p.table[w.x * p.table_st + m];
     };
     if (group == 1 && share > 1) advance();
     lookup();
@@ -779,7 +779,7 @@ struct SlotMap {
       m = __umulhi(uint32_t(j), p.page_magic);  // j / per_page, or one more
       if (int64_t(m) * p.per_page > j) --m;
     }
-    const int page = __ldg(table + m);
+    const int page = table[m];
     if (page < 0 || page >= p.pages) {
       if (p.err_word != nullptr) atomicOr(p.err_word, QSA_ERRBIT_SLOT_RANGE);
       return -1;
@@ -808,7 +808,7 @@ __device__ __forceinline__ void list_slots(const SlotMap& map, int* list, int n,
         if (int64_t(m) * p.per_page > j) --m;
       }
       off[u] = (j - m * p.per_page) * p.block;
-      page[u] = __ldg(map.table + m);
+      page[u] = map.table[m];
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -1029,7 +1029,7 @@ __global__ void __launch_bounds__(32 * kPickWarps) qsa_select_pick_kernel(const 
     for (int i = 0; i * 128 < f; ++i) {
       const int j = i * 128 + lane * 4;
       uint4 k = make_uint4(0u, 0u, 0u, 0u);
-      if (j < f) k = __ldg(row4 + i * 32);
+      if (j < f) k = load_l2(row4 + i * 32);
       k = make_uint4(order_key(k.x), order_key(k.y), order_key(k.z), order_key(k.w));
       if (i * 128 < p.sink || i * 128 + 128 > f - p.local) {
         if (forced(j)) k.x = 0u;  // (or past the end)
@@ -1142,10 +1142,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : THREADS == 256 
     const int want = p.top - p.sink - p.local;
     auto forced = [&](int j) { return j < p.sink || j >= f - p.local; };
     auto searched = [&](int j, uint32_t score) { return forced(j) ? 0u : order_key(score); };
-    auto in_row = [&](int j) { return searched(j, __float_as_uint(__ldg(row + j))); };
+    auto in_row = [&](int j) { return searched(j, __float_as_uint(load_l2(row + j))); };
     const uint4* row4 = reinterpret_cast<const uint4*>(row);  // (ld is a multiple of 32)
     auto four_in_row = [&](int i) {  // (past the end: not searched)
-      const uint4 k = __ldg(row4 + i);
+      const uint4 k = load_l2(row4 + i);
       return make_uint4(searched(4 * i, k.x), searched(4 * i + 1, k.y), searched(4 * i + 2, k.z),
                         searched(4 * i + 3, k.w));
     };
@@ -1159,7 +1159,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : THREADS == 256 
         uint4 k[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u)
-          if ((i0 + u * THREADS) * 4 < f) k[u] = __ldg(row4 + i0 + u * THREADS);
+          if ((i0 + u * THREADS) * 4 < f) k[u] = load_l2(row4 + i0 + u * THREADS);
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
           const int j = (i0 + u * THREADS) * 4;
@@ -1207,7 +1207,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : THREADS == 256 
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
               next[u] = make_uint4(0u, 0u, 0u, 0u);
-              if ((i0 + lane + u * THREADS) * 4 < f) next[u] = __ldg(row4 + i0 + lane + u * THREADS);
+              if ((i0 + lane + u * THREADS) * 4 < f) next[u] = load_l2(row4 + i0 + lane + u * THREADS);
             }
           };
           load(s0 + warp * 32);
@@ -1260,7 +1260,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : THREADS == 256 
           break;
         }
 #pragma unroll 4
-        for (int i = tid; i < room; i += THREADS) sKey[i] = order_key(__float_as_uint(__ldg(row + sIdx[i])));
+        for (int i = tid; i < room; i += THREADS) sKey[i] = order_key(__float_as_uint(load_l2(row + sIdx[i])));
         if (tid < 4 && room + tid < (room + 3) / 4 * 4) sKey[room + tid] = 0u;
         border = kth_largest<THREADS, true>((room + 3) / 4, want, four_in_list, sh);
         if (n == room) {
