@@ -84,3 +84,79 @@ def test_index_keys_and_selection_in_turn():
     torch.cuda.synchronize()
     for n, (idx, width) in enumerate(got):
         assert torch.equal(idx, want[n % 3][0]) and torch.equal(width, want[n % 3][1])
+
+
+# ---- the score's roundings --------------------------------------------------------------------
+
+def plain_select(s, top, rows_at_once=512):
+    """select_slots of one sequence in elementary torch operations, every row: the products of
+    codes exact (below 2^24), every other product and sum rounded to 32 bits, heads in order."""
+    q, block, page = s["q"], s["block"], s["page_size"]
+    Tq, Hi, _ = q.shape
+    per, n = page // block, int(s["seq_lens"][0])
+
+    def codes_of(x):
+        step = x.abs().amax(-1, keepdim=True) / torch.full((), 127.0, device="cuda")
+        return torch.where(step > 0, torch.round(x / step), 0.0), step.squeeze(-1)
+
+    code, step = codes_of(q.float())
+    gain = s["weight"] * step
+    where = (s["page_table"][0].long()[:, None] * per + torch.arange(per, device="cuda")).flatten()
+    key, scale = s["codes"][where].double(), s["scales"][where]
+    j = torch.arange(where.numel(), device="cuda")
+    W = top * block + block - 1
+    idx, width = torch.full((Tq, W), -1, dtype=I32, device="cuda"), torch.empty(Tq, dtype=I32, device="cuda")
+    for t0 in range(0, Tq, rows_at_once):
+        t = torch.arange(t0, min(Tq, t0 + rows_at_once), device="cuda")
+        seen = (n - (Tq - 1 - t)).clamp(min=0)
+        f = (seen // block)[:, None]
+        dot = (code[t].double().flatten(0, 1) @ key.T).clamp(min=0).float().view(t.numel(), Hi, -1)
+        total = gain[t, 0, None] * dot[:, 0]
+        for h in range(1, Hi):
+            total = total + gain[t, h, None] * dot[:, h]
+        score = (total * scale).masked_fill(j >= f, float("-inf"))
+        best = score.sort(dim=-1, descending=True, stable=True).indices[:, :top]
+        best = torch.where(torch.arange(best.shape[1], device="cuda") < f, best, where.numel()).sort(-1).values
+        taken = torch.minimum(f, torch.tensor(top, device="cuda"))
+        slots = torch.cat([where, where.new_zeros(1)])[best][..., None] * block + torch.arange(block, device="cuda")
+        idx[t, :slots.shape[1] * block] = slots.masked_fill((best == where.numel())[..., None], -1).flatten(1).to(I32)
+        for e in range(block - 1):  # the incomplete block
+            row = (e < seen - f[:, 0] * block).nonzero().flatten()
+            idx[t[row], (taken[row, 0] * block + e)] = (where[f[row, 0]] * block + e).to(I32)
+        width[t] = (taken[:, 0] * block + seen % block).to(I32)
+    return idx, width
+
+
+def test_select_every_row_of_a_long_prefill():
+    """Of 7,810 rows over 16,384 blocks some have their border between scores a step apart."""
+    for seed in range(230, 238):
+        s = select_state(seed, *LONG)
+        idx, width = qsa.select_slots(**s, top_blocks=512)
+        want_idx, want_width = plain_select(s, 512)
+        assert torch.equal(width, want_width)
+        assert torch.equal(idx, want_idx), f"{int((idx != want_idx).any(1).sum())} rows differ"
+
+
+@pytest.mark.parametrize("Hi", [1, 2, 3, 4, 7, 8, 16, 23, 32, 40, 64])
+@pytest.mark.parametrize("Di", [64, 128])
+def test_select_scores_a_step_apart(Hi, Di):
+    """Blocks whose scores are 1 to within eight 32-bit steps: their order, and the choice, hang on
+    every single rounding.  Many rows of a sequence and the same rows as sequences of their own."""
+    n, rows = 700, 150
+    s = select_state(240, [4 * n + 3], [rows], Hi, Di)
+    s["q"] = s["q"][:1].expand(rows, Hi, Di).contiguous()
+    s["weight"] = s["weight"][:1].abs().expand(rows, Hi).contiguous()  # (positive: no cancellation)
+    where = (s["page_table"][0].long()[:, None] * 16 + torch.arange(16, device="cuda")).flatten()
+    code, step = ref.codes_of(s["q"][0].float().cpu().numpy())
+    gain = s["weight"][0].double() * torch.from_numpy(step).cuda().double()
+    total = ((torch.from_numpy(code).cuda().double() @ s["codes"][where].double().T).clamp(min=0) * gain[:, None]).sum(0)
+    wobble = 1 + torch.randint(0, 8, total.shape, generator=gen(241), device="cuda") * 2.0 ** -23
+    s["scales"][where] = torch.where(total > 0, wobble / total, 1.0).float()
+    top = 200
+    want_idx, want_width = plain_select(s, top)
+    idx, width = qsa.select_slots(**s, top_blocks=top)
+    assert torch.equal(idx, want_idx) and torch.equal(width, want_width)
+    alone = dict(s, cu_q=None, page_table=s["page_table"].expand(rows, -1).contiguous(),
+                 seq_lens=4 * n + 3 - (rows - 1) + torch.arange(rows, device="cuda", dtype=I32))
+    idx, width = qsa.select_slots(**alone, top_blocks=top)
+    assert torch.equal(idx, want_idx) and torch.equal(width, want_width)

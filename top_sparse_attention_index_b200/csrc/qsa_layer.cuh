@@ -192,7 +192,9 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
-// Two floats per instruction, each operation rounded as the scalar one.
+// Two floats per instruction, each operation rounded as the scalar one; but the compiler fuses
+// a mul2 and the add2 of its result, .rn or not: where a product has to be rounded by itself
+// before a sum, it is an fma2 with +0.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(lo), "f"(hi));

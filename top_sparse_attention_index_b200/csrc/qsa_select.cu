@@ -720,8 +720,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int col = c * 32 + x + 2 * e, head = (col % (2 * HP)) >> 1, pair = col / (2 * HP);
-            const uint64_t term = mul2(add2(pack2(f[2 * e], f[2 * e + 1]), minus),
-                                       e == 0 ? pack2(g.x, g.y) : pack2(g.z, g.w));
+            // (a product rounded by itself: written as mul2, it and the sum's add2 became one fused
+            // operation, packed .rn instructions or not, and 17 % of four-head scores came out a step off)
+            const uint64_t term = fma2(add2(pack2(f[2 * e], f[2 * e + 1]), minus),
+                                       e == 0 ? pack2(g.x, g.y) : pack2(g.z, g.w), zero);
             sum = head == 0 ? term : add2(sum, term);
             if (head == HP - 1) {
               float s[2];
