@@ -7,7 +7,8 @@ import torch
 
 import layer_reference as ref
 import top_sparse_attention_index_b200 as qsa
-from test_layer_gpu import BF, F8, I32, err_word, gen, normal
+from test_layer_gpu import (BF, F8, I32, check_select, close, decode_case, err_word, gen, keyed_case, normal,
+                            run_select, select_case)
 
 pytestmark = pytest.mark.gpu
 
@@ -160,3 +161,53 @@ def test_select_scores_a_step_apart(Hi, Di):
                  seq_lens=4 * n + 3 - (rows - 1) + torch.arange(rows, device="cuda", dtype=I32))
     idx, width = qsa.select_slots(**alone, top_blocks=top)
     assert torch.equal(idx, want_idx) and torch.equal(width, want_width)
+
+
+# ---- scores of no size ------------------------------------------------------------------------
+
+def zeros_case(n, rows):
+    """`rows` rows of one sequence of n blocks: scores of +0, of a negative product that underflows
+    (-0), and a few below zero; all zeros are equal, so the lower blocks win."""
+    c = keyed_case(torch.ones(n, device="cuda"), rows, 0)
+    c["weight"].fill_(-1e-10)
+    kind = torch.randint(0, 5, c["scales"].shape, generator=gen(250), device="cuda")
+    c["scales"] = torch.tensor([0.0, 1e-40, 0.0, 1e-40, 1.0], device="cuda")[kind]
+    return c
+
+
+@pytest.mark.parametrize("rows,n", [(1, 700), (150, 700), (1300, 700), (1, 40000), (200, 40000), (1300, 40000)])
+def test_select_zeros_of_both_signs_are_equal(rows, n):
+    """In both forms of the score, and in the choice of short and long rows; of the long ones more
+    blocks share the border than are collected."""
+    c = zeros_case(n, rows)
+    if n == 700 and rows == 1300:  # rows of at most 2,048 blocks, a warp each
+        c["seq_lens"] += rows
+        c["page_table"] = torch.cat([c["page_table"], c["page_table"][:, :1].expand(1, 21)], 1).contiguous()
+    for top, sink, local in ((100, 0, 0), (500, 1, 7)):
+        got, width = run_select(c, top, sink, local)
+        for t in sorted({0, rows // 2, rows - 1}):
+            want, want_width = ref.select(c["q"][t:t + 1], c["weight"][t:t + 1], c["codes"], c["scales"],
+                                          c["page_table"], c["seq_lens"] - (rows - 1 - t), None, top,
+                                          c["page_size"], 1, sink, local)
+            assert torch.equal(got[t].cpu(), torch.from_numpy(want[0])) and int(width[t]) == int(want_width[0])
+
+
+def test_select_scores_that_underflow():
+    """Scores of both signs from 2^-130 down, subnormal ones and zeros among them."""
+    for rows in (None, [140, 70]):
+        c = select_case(251, [3000, 2500], rows, 4, 128, 4, 64)
+        c["weight"] = (c["weight"] * 1e-10).contiguous()
+        c["scales"] = torch.exp2(-100 - 30 * torch.rand(c["scales"].shape, generator=gen(252), device="cuda"))
+        assert check_select(c, 100) == 0 and check_select(c, 500, 1, 3) == 0
+
+
+def test_select_ignores_what_the_workspace_held():
+    """The score's room full of NaNs of both signs, infinities and -0 before the call."""
+    c = select_case(253, [3000, 2500], [140, 3], 4, 128, 4, 64)
+    P = c["page_table"].shape[1]
+    work = torch.empty(qsa.qsa_select_slots_workspace_bytes(143, 2, P, 64, 4, 128, 4), dtype=torch.uint8, device="cuda")
+    want, want_width = run_select(c, 100)
+    for bits in (0x7fffffff, -1, 0x7f800000, -2 ** 31):
+        work[:work.numel() // 4 * 4].view(I32).fill_(bits)
+        got, width = run_select(c, 100, workspace=work)
+        assert torch.equal(got, want) and torch.equal(width, want_width)

@@ -37,17 +37,20 @@ struct SelectParams {
 };
 
 // The score as it is kept: a NaN (of the codes or weights, or the scale of a block whose page
-// lies outside the pool) counts as -infinity, -0 as +0.
+// lies outside the pool) counts as -infinity.  (Adding +0 spares most zeros their sign, but a
+// negative product that underflows is -0.)
 __device__ __forceinline__ float kept_score(float sum, float scale) {
   return fmaxf(__fmaf_rn(sum, scale, 0.f), -__builtin_huge_valf());
 }
 
-// The order of scores as an order of unsigned integers, -infinity at kLeastKey and nothing (not
-// what a failed score kernel left, either) below it; 0 is left for blocks that take no part.
+// The order of scores as an order of unsigned integers: both zeros the same, -infinity, and
+// with it any NaN that a failed score kernel left, at kLeastKey and nothing below it; 0 is
+// left for blocks that take no part.  So keys compare as the scores do, whatever their bits.
 // And back.
 constexpr uint32_t kLeastKey = 0x007fffffu;
-__device__ __forceinline__ uint32_t order_key(uint32_t score) {
-  return max(score ^ (uint32_t(int32_t(score) >> 31) | 0x80000000u), kLeastKey);
+__device__ __forceinline__ uint32_t order_key(uint32_t bits) {
+  const uint32_t score = __float_as_uint(fmaxf(__fadd_rn(__uint_as_float(bits), 0.f), -__builtin_huge_valf()));
+  return score ^ (uint32_t(int32_t(score) >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float key_score(uint32_t key) {
   key = max(key, kLeastKey);
@@ -727,7 +730,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             sum = head == 0 ? term : add2(sum, term);
             if (head == HP - 1) {
               float s[2];
-              unpack2(fma2(sum, scale2, zero), s[0], s[1]);  // (-0 becomes +0)
+              unpack2(fma2(sum, scale2, zero), s[0], s[1]);  // (as kept_score)
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
                 if (2 * pair + k < rows) p.scores[at] = fmaxf(s[k], -__builtin_huge_valf());  // (NaN: -infinity)
@@ -1194,7 +1197,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : THREADS == 256 
       uint16_t* queue = reinterpret_cast<uint16_t*>(sKey);
       const int longest = p.queue / THREADS;
       constexpr int kStep = THREADS * kBatch;  // 16-byte loads of a step
-      int tied = 0;  // keys from low - 1 up, when the want-th largest of some of them is low - 1
+      bool tied = false;  // the want-th largest of some of the keys is low - 1
       bool found = false;
       for (int tries = 0; tries < 3; ++tries) {
         __syncthreads();
@@ -1258,7 +1261,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : THREADS == 256 
         const int n = sh.n, room = min(have, p.cap);
         if (room < want) {
           // above a key that more share than there is room for: that one is the border
-          if (tied > 0 && n < want) border = {low - 1u, want - n, tied - n}, found = true;
+          // (a number of equal ones that is never `want`: the first of them are counted off)
+          if (tied && n < want) border = {low - 1u, want - n, INT32_MAX}, found = true;
           break;
         }
 #pragma unroll 4
@@ -1269,8 +1273,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : THREADS == 256 
           listed = n;
           break;
         }
-        tied = border.key <= low ? n : 0;
-        low = tied > 0 ? low + 1u : border.key;
+        tied = border.key <= low;
+        low = tied ? low + 1u : border.key;
       }
       if (listed < 0 && !found) border = kth_largest<THREADS, true>((f + 3) / 4, want, four_in_row, sh);
     }
