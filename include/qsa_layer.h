@@ -133,6 +133,8 @@ qsa_status_t qsa_pack_index_keys(const void* keys, int64_t key_stride_s, const i
  *               as -1.
  *   seq_lens    int32 [B]; values outside [0, P page_size] are clamped and set
  *               QSA_ERRBIT_WIDTH_RANGE, as do values of cu_q outside [0, Tq].
+ *   cu_q        int32 [B + 1], non-decreasing.  One that decreases sets
+ *               QSA_ERRBIT_WIDTH_RANGE, and the rows are not valid: slots of the pool, or -1.
  *   1 <= Hi <= 64, Di 64 or 128, block 1..16, top_blocks >= 1 with top_blocks * block <= 8192,
  *   sink_blocks + local_blocks <= top_blocks.
  *   workspace   qsa_select_slots_workspace_bytes(...) bytes, 256-byte aligned.

@@ -211,3 +211,18 @@ def test_select_ignores_what_the_workspace_held():
         work[:work.numel() // 4 * 4].view(I32).fill_(bits)
         got, width = run_select(c, 100, workspace=work)
         assert torch.equal(got, want) and torch.equal(width, want_width)
+
+
+@pytest.mark.parametrize("cu", [[0, 60, 20, 100], [0, 3, 1, 4], [0, 300] + [0, 300] * 6, [300, 0, 300]])
+def test_select_offsets_that_decrease_are_reported(cu):
+    """Sequences that share rows: an error bit, and nothing outside the pool."""
+    B, Tq = len(cu) - 1, max(cu)
+    c = select_case(254, [3000] * B, [-(-Tq // B)] * B, 4, 128, 4, 64)
+    c["q"], c["weight"] = c["q"][:Tq], c["weight"][:Tq]
+    c["cu_q"] = torch.tensor(cu, dtype=I32, device="cuda")
+    err = err_word()
+    idx, width = run_select(c, 100, err_word=err)
+    assert int(err) == qsa.QSA_ERRBIT_WIDTH_RANGE
+    in_use = width >= 0  # (a row of no sequence keeps -7)
+    assert (idx[in_use] >= -1).all() and (idx < c["codes"].shape[0] * 4).all()
+    assert (width[in_use] <= 403).all() and in_use.sum() > 0

@@ -61,7 +61,7 @@ __device__ __forceinline__ float key_score(uint32_t key) {
 __device__ __forceinline__ int2 rows_of(const SelectParams& p, int b, bool report) {
   if (p.cu == nullptr) return make_int2(b, b + 1);
   int lo = p.cu[b], hi = p.cu[b + 1];
-  if (report && p.err_word != nullptr && (lo < 0 || lo > p.Tq || hi < 0 || hi > p.Tq))
+  if (report && p.err_word != nullptr && (lo < 0 || lo > p.Tq || hi < lo || hi > p.Tq))
     atomicOr(p.err_word, QSA_ERRBIT_WIDTH_RANGE);
   lo = min(max(lo, 0), p.Tq);
   hi = min(max(hi, 0), p.Tq);
