@@ -34,9 +34,9 @@ extern "C" {
 #define QSA_MAX_INDEX_HEADS 64
 #define QSA_MAX_TOP_BLOCKS 8192
 
-/* A further bit of *err_word: a bounded wait of qsa_select_slots for its own copies or
- * products ran out (the device was stopped or is failing); the output is not
- * valid. */
+/* A further bit of *err_word: a bounded wait (one second) of qsa_select_slots for its own
+ * copies or products ran out (the device was stopped or is failing).  The rows whose scores
+ * were computed with those come out empty: a width of 0, and -1 for every slot. */
 #define QSA_ERRBIT_TIMEOUT 0x10u
 
 /*

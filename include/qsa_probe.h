@@ -1,5 +1,5 @@
 /*
- * qsa_probe.h -- measurement entry point of libqsa.so: the gather-rate probe.
+ * qsa_probe.h -- measurement and test entry points of libqsa.so.  First the gather-rate probe.
  *
  * Not part of the attention computation.  It measures, on the device at hand, the
  * SM-side roofline of the sparse-attention gather: how fast the SMs pull rows chosen at
@@ -96,6 +96,14 @@ qsa_status_t qsa_probe_gather(int32_t method, int32_t read_back, const void* src
  */
 qsa_status_t qsa_probe_mma_operands(int32_t method, int32_t n, int32_t rounds, int32_t ctas,
                                     int64_t* out, void* stream);
+
+/*
+ * qsa_probe_select_wait_ns -- sets the limit of each bounded wait of qsa_select_slots'
+ * tcgen05 score (calls after it, of the whole process) and returns the one before; one second
+ * unless set.  For tests of what a call leaves when a wait runs out (QSA_ERRBIT_TIMEOUT): with
+ * a limit below the copies' latency the waits of a healthy device do.
+ */
+uint32_t qsa_probe_select_wait_ns(uint32_t ns);
 
 #ifdef __cplusplus
 }

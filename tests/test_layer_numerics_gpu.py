@@ -226,3 +226,34 @@ def test_select_offsets_that_decrease_are_reported(cu):
     in_use = width >= 0  # (a row of no sequence keeps -7)
     assert (idx[in_use] >= -1).all() and (idx < c["codes"].shape[0] * 4).all()
     assert (width[in_use] <= 403).all() and in_use.sum() > 0
+
+
+# ---- waits that run out -----------------------------------------------------------------------
+
+@pytest.mark.parametrize("rows", [[300, 140], [1500, 9]])
+def test_select_waits_that_run_out(rows):
+    """The tcgen05 score with a limit of its waits below the latency of what they wait for: the call
+    ends, its rows are empty and the error word says so, and the next call is right."""
+    c = select_case(260, [6000, 5000], rows, 4, 128, 4, 64)
+    want, want_width = run_select(c, 100)
+    torch.cuda.synchronize()
+    lib = qsa.load_library()
+    late = 0
+    for ns in (0, 0, 100, 300, 1000, 3000, 10000, 30000):
+        before = lib.qsa_probe_select_wait_ns(ns)
+        try:
+            err = err_word()
+            got, width = run_select(c, 100, err_word=err)
+            torch.cuda.synchronize()
+        finally:
+            lib.qsa_probe_select_wait_ns(before)
+        assert before == 10 ** 9
+        if int(err) == qsa.QSA_ERRBIT_TIMEOUT:
+            late += 1
+            assert (got == -1).all() and (width == 0).all()
+        else:
+            assert int(err) == 0 and torch.equal(got, want) and torch.equal(width, want_width)
+        err = err_word()
+        got, width = run_select(c, 100, err_word=err)
+        assert int(err) == 0 and torch.equal(got, want) and torch.equal(width, want_width)
+    assert late > 0

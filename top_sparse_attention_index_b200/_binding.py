@@ -59,6 +59,7 @@ SIGNATURES = {
     "qsa_probe_gather": (_i32, [_i32, _i32, _p, _i64, _i64, _i32, _i32, _i32, _i32, _i32,
                                 ctypes.c_uint32, _p, _p]),
     "qsa_probe_mma_operands": (_i32, [_i32, _i32, _i32, _i32, _p, _p]),
+    "qsa_probe_select_wait_ns": (ctypes.c_uint32, [ctypes.c_uint32]),
     "qsa_combine_peer_records": (_i32, [ctypes.POINTER(_p), ctypes.POINTER(_p), _i32, _i32, _i32,
                                         _i32, _i32, _i32, _i32, ctypes.POINTER(_p), _i32, _i64,
                                         _i64, _p]),

@@ -161,25 +161,27 @@ __device__ __forceinline__ uint64_t clock_ns() {
   return t;
 }
 
-// Waits for a phase of an mbarrier, one second at most; false when it has not come by then.
+// Waits for a phase of an mbarrier, `limit` ns at most; false when it has not come by then.
 // The hint lets the hardware hold the thread for up to 100 us, or until the phase completes,
 // instead of a few cycles: waiting warps would otherwise take issue slots from working ones.
-__device__ __forceinline__ bool poll_phase(uint32_t bar, uint32_t parity) {
+constexpr uint32_t kWaitLimit = 1000000000u;  // one second
+__device__ __forceinline__ bool poll_phase(uint32_t bar, uint32_t parity, uint32_t hint) {
   uint32_t done;
   asm volatile(
       "{\n  .reg .pred p;\n  mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
       "  selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(done)
-      : "r"(bar), "r"(parity), "r"(100000u)
+      : "r"(bar), "r"(parity), "r"(hint)
       : "memory");
   return done != 0;
 }
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity) {
-  if (poll_phase(bar, parity)) return true;
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, uint32_t limit = kWaitLimit) {
+  const uint32_t hint = min(limit, 100000u);
+  if (poll_phase(bar, parity, hint)) return true;
   const uint64_t start = clock_ns();
   do {
-    if (poll_phase(bar, parity)) return true;
-  } while (clock_ns() - start < 1000000000u);
+    if (poll_phase(bar, parity, hint)) return true;
+  } while (clock_ns() - start < limit);
   return false;
 }
 

@@ -6,6 +6,9 @@
 // into the workspace, the choice kernel finds the border of each row's top_blocks best and
 // writes the slots of the blocks above it.
 #include "qsa_layer.cuh"
+#include "qsa_probe.h"
+
+#include <atomic>
 
 namespace {
 
@@ -16,6 +19,7 @@ constexpr int kScoreThreads = 256;
 constexpr int kScoreBlocks = 2;               // of an SM
 constexpr int64_t kChunkBytes = 512 << 20;    // most scores of one chunk of rows
 constexpr int kMinChunkRows = 64;
+constexpr int32_t kLate = 1 << 30;            // of a tile's number of rows (at most 256): see SelectParams
 
 struct SelectParams {
   const uint16_t* q;
@@ -31,6 +35,8 @@ struct SelectParams {
   int32_t Tq, B, P, page_size, per_page, Hi, block, top, sink, local;
   int4* tiles;         // tcgen05 form: tiles of rows [chunks, max_tiles], and their codes and gains
   uint8_t* tile_q;
+  int32_t* late;       // tcgen05 form: a word of the chunk's first tile, kLate set when a wait ran out
+  uint32_t wait_ns;    // limit of each such wait
   int32_t first;       // the choice is the call's first kernel
   int32_t cap, queue, window;              // keys of a row, and words of its marks, in the choice's shared memory
   uint32_t page_magic, block_magic; // 2^32 / per_page (/ block), rounded up
@@ -404,7 +410,7 @@ __global__ void __launch_bounds__(256) qsa_select_prep_kernel(const SelectParams
   const int tile = blockIdx.x / kPrepParts, part = blockIdx.x % kPrepParts;
   const WideTile w = find_tile<256>(p, c0, c1, tile, kWideCols / HP, sTmp, sFound);
   const int64_t slot = int64_t(blockIdx.y) * (gridDim.x / kPrepParts) + tile;
-  if (threadIdx.x == 0 && part == 0) p.tiles[slot] = make_int4(w.b, w.t0, w.n, w.b < 0 ? 0 : w.f);
+  if (threadIdx.x == 0 && part == 0) p.tiles[slot] = w.b < 0 ? make_int4(-1, 0, 0, 0) : make_int4(w.b, w.t0, w.n, w.f);
   if (w.b < 0 || w.f == 0) return;
   uint8_t* dst = p.tile_q + slot * wide_tile_bytes(DI);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % kLanes;
@@ -497,7 +503,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   // key stage full / free, Q full / free, accumulator full / free
   __shared__ __align__(8) uint64_t sBar[2 * kWideStages + 2 * kWideQ + 4];
   __shared__ uint32_t sTmem;
-  __shared__ int sTmp[kWideThreads / 32], sStart[2];
+  __shared__ int sTmp[kWideThreads / 32], sStart[2], sLoaded[kWideQ];  // the last Q tile in each place
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto bar = [&](int i) { return smem_addr(sBar + i); };
   constexpr int kFull = 0, kFree = kWideStages, kQFull = 2 * kWideStages, kQFree = kQFull + kWideQ,
@@ -528,6 +534,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       mbar_init(bar(kFree + i), 1 + kEpilogueWarps);
     }
     for (int i = 0; i < kWideQ; ++i) {
+      sLoaded[i] = -1;
       mbar_init(bar(kQFull + i), 1);
       mbar_init(bar(kQFree + i), 1 + kEpilogueWarps);
     }
@@ -548,7 +555,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   const int tile0 = sStart[0], first_kt = sStart[1];
   const int share = int(u1 - u0);
   bool late = false;
-  int q_loaded = -1;  // (the first thread of a producer group) the last Q tile it loaded
 
   if (warp >= kEpilogueWarps && warp < kEpilogueWarps + kProducerWarps) {
     // ---- producers: two groups take the key tiles in turn, one key row per thread ----------------
@@ -600,15 +606,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         lookup();
       }
       const int stage = i % kWideStages;
-      if (i >= kWideStages && !wait_phase(bar(kFree + stage), (i / kWideStages - 1) & 1)) late = true;
+      if (i >= kWideStages && !wait_phase(bar(kFree + stage), (i / kWideStages - 1) & 1, p.wait_ns)) late = true;
       if (load_q && r == 0 && !late) {
         const int qb = this_q % kWideQ;
-        if (this_q >= kWideQ && !wait_phase(bar(kQFree + qb), (this_q / kWideQ - 1) & 1)) late = true;
+        if (this_q >= kWideQ && !wait_phase(bar(kQFree + qb), (this_q / kWideQ - 1) & 1, p.wait_ns)) late = true;
         if (!late) {
           mbar_arrive_expect_tx(bar(kQFull + qb), C::kQBytes);
           bulk_copy(smem_addr(sQ) + qb * C::kQBytes, tile_q + int64_t(this_tile) * C::kQBytes, C::kQBytes,
                     bar(kQFull + qb));
-          q_loaded = this_q;
+          atomicMax(&sLoaded[qb], this_q);
         }
       }
       if (late) break;
@@ -642,9 +648,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       int i = 0;
       for (; i < share; ++i) {
         const int stage = i % kWideStages, acc = i & 1;
-        if (new_q) late = !wait_phase(bar(kQFull + qn % kWideQ), (qn / kWideQ) & 1);
-        if (!late) late = !wait_phase(bar(kFull + stage), (i / kWideStages) & 1);
-        if (!late && i >= 2) late = !wait_phase(bar(kAccFree + acc), ((i >> 1) - 1) & 1);
+        if (new_q) late = !wait_phase(bar(kQFull + qn % kWideQ), (qn / kWideQ) & 1, p.wait_ns);
+        if (!late) late = !wait_phase(bar(kFull + stage), (i / kWideStages) & 1, p.wait_ns);
+        if (!late && i >= 2) late = !wait_phase(bar(kAccFree + acc), ((i >> 1) - 1) & 1, p.wait_ns);
         if (late) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t a = smem_addr(smem) + stage * C::kKeyBytes, q = smem_addr(sQ) + (qn % kWideQ) * C::kQBytes;
@@ -686,10 +692,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     for (int i = 0; i < share; ++i) {
       const int stage = i % kWideStages, acc = i & 1;
       // (the key stage and the Q tile landed before their product: these waits order the reads)
-      bool here = wait_phase(bar(kFull + stage), (i / kWideStages) & 1);
-      if (new_q) here = here && wait_phase(bar(kQFull + qn % kWideQ), (qn / kWideQ) & 1);
+      bool here = wait_phase(bar(kFull + stage), (i / kWideStages) & 1, p.wait_ns);
+      if (new_q) here = here && wait_phase(bar(kQFull + qn % kWideQ), (qn / kWideQ) & 1, p.wait_ns);
       new_q = false;
-      here = here && wait_phase(bar(kAccFull + acc), (i >> 1) & 1);
+      here = here && wait_phase(bar(kAccFull + acc), (i >> 1) & 1, p.wait_ns);
       if (__any_sync(0xffffffffu, !here)) {
         late = true;
         break;
@@ -701,7 +707,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const float* gains = reinterpret_cast<const float*>(sQ + (qn % kWideQ) * C::kQBytes + kWideCols * DI) + part * kPartCols;
       const int row0 = part * kPartRows;
       uint32_t at = uint32_t(w.y + row0 - p.c0) * uint32_t(p.ld) + uint32_t(j);  // (a chunk has fewer than 2^30)
-      const int rows = j < p.ld ? w.z - row0 : 0;  // that this lane stores
+      const int rows = j < p.ld ? (w.z & (kLate - 1)) - row0 : 0;  // that this lane stores
       const uint64_t minus = pack2(-8388608.f, -8388608.f), zero = pack2(0.f, 0.f);
       uint64_t sum = zero;
 #pragma unroll
@@ -752,11 +758,16 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       }
     }
   }
-  // (every Q tile's copy has landed when its product was issued, unless a wait ran out)
+  // A wait that ran out leaves scores unwritten: the choice gives the chunk's rows no slots.  No
+  // product and no copy of a thread of its own is in flight here; the bulk copies of Q tiles have
+  // landed when their product was issued, or are waited for now (one second at most).
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   if (__syncthreads_or(late)) {
-    if (late && p.err_word != nullptr) atomicOr(p.err_word, QSA_ERRBIT_TIMEOUT);
-    if (q_loaded >= 0) wait_phase(bar(kQFull + q_loaded % kWideQ), (q_loaded / kWideQ) & 1);  // a second chance
+    if (late) {
+      atomicOr(p.late, kLate);
+      if (p.err_word != nullptr) atomicOr(p.err_word, QSA_ERRBIT_TIMEOUT);
+    }
+    if (tid < kWideQ && sLoaded[tid] >= 0) wait_phase(bar(kQFull + tid), (sLoaded[tid] / kWideQ) & 1);
     __syncthreads();
   }
   if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
@@ -824,6 +835,10 @@ __device__ __forceinline__ void list_slots(const SlotMap& map, int* list, int n,
   }
   if (bad && p.err_word != nullptr) atomicOr(p.err_word, QSA_ERRBIT_SLOT_RANGE);
 }
+
+// Whether the chunk's scores are not whole (read after the score kernel's end): the choice then
+// goes on as if its rows saw nothing.
+__device__ __forceinline__ bool scores_late(const SelectParams& p) { return p.late != nullptr && (*p.late & kLate) != 0; }
 
 // Row t's output from the first slots of its taken blocks, by THREADS threads.
 template <int THREADS>
@@ -1020,8 +1035,8 @@ __global__ void __launch_bounds__(32 * kPickWarps) qsa_select_pick_kernel(const 
     return;
   }
   const int last = rows_of(p, b, false).y - 1, len = length_of(p, b, lane == 0);
-  const int seen = max(len - (last - t), 0), f = seen / p.block, taken = min(f, p.top);
   wait_for_last();  // the scores
+  const int seen = scores_late(p) ? 0 : max(len - (last - t), 0), f = seen / p.block, taken = min(f, p.top);
   const SlotMap map{p, p.table + b * p.table_st};
   if (f <= p.top) {
     for (int j = lane; j < f; j += 32) sList[j] = map.first_slot(j);
@@ -1135,9 +1150,9 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : THREADS == 256 
     return;
   }
   const int last = rows_of(p, b, false).y - 1, len = length_of(p, b, tid == 0);
-  const int seen = max(len - (last - t), 0);
-  const int f = seen / p.block, taken = min(f, p.top);
   wait_for_last();  // the scores
+  const int seen = scores_late(p) ? 0 : max(len - (last - t), 0);
+  const int f = seen / p.block, taken = min(f, p.top);
   const float* row = p.scores + blockIdx.x * p.ld;
   const SlotMap map{p, p.table + b * p.table_st};
   if (f <= p.top) {
@@ -1405,6 +1420,8 @@ cudaError_t launch_prep(const SelectParams& p, int chunk_rows, int chunks, cudaS
   return launch(qsa_select_prep_kernel<DI, HP>, grid, 256, 0, st, p, chunk_rows);
 }
 
+std::atomic<uint32_t> g_wait_ns{kWaitLimit};  // see qsa_probe_select_wait_ns
+
 template <int DI, int HP>
 cudaError_t launch_wide(const SelectParams& p, int chunk, int chunk_rows, int num_sms, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(qsa_select_wide_kernel<DI, HP>,
@@ -1529,6 +1546,8 @@ qsa_status_t check_select_sizes(int32_t Tq, int32_t B, int32_t P, int32_t page_s
 
 }  // namespace
 
+extern "C" uint32_t qsa_probe_select_wait_ns(uint32_t ns) { return g_wait_ns.exchange(ns); }
+
 extern "C" size_t qsa_select_slots_workspace_bytes(int32_t Tq, int32_t B, int32_t P, int32_t page_size,
                                                    int32_t Hi, int32_t Di, int32_t block) {
   set_error_detail("%s", "");
@@ -1603,6 +1622,7 @@ extern "C" qsa_status_t qsa_select_slots(
   p.block_magic = uint32_t(((uint64_t(1) << 32) + block - 1) / block);
   p.first = ld <= top_blocks;
   const bool scored = !p.first;  // (a table of at most top_blocks blocks needs no scores)
+  p.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
   auto wide_launch = [&](int chunk) {
     return Di == 128 ? launch_wide_for<128>(p, chunk, rows, lay.chunks, num_sms, st)
                      : launch_wide_for<64>(p, chunk, rows, lay.chunks, num_sms, st);
@@ -1615,6 +1635,7 @@ extern "C" qsa_status_t qsa_select_slots(
     const int64_t c0 = int64_t(chunk) * rows;
     p.c0 = int32_t(c0);
     p.c1 = int32_t(c0 + rows < Tq ? c0 + rows : Tq);
+    if (scored && wide) p.late = &p.tiles[chunk * wide_max_tiles(rows, B, Hi)].z;
     if (scored) {
       e = wide ? wide_launch(chunk)
           : Di == 128 ? launch_score_for<128>(p, num_sms, st) : launch_score_for<64>(p, num_sms, st);
