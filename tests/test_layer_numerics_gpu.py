@@ -2,6 +2,8 @@
 calls that follow each other without a pause, scores a step apart, exact counts of slots."""
 from __future__ import annotations
 
+import threading
+
 import pytest
 import torch
 
@@ -257,3 +259,53 @@ def test_select_waits_that_run_out(rows):
         got, width = run_select(c, 100, err_word=err)
         assert int(err) == 0 and torch.equal(got, want) and torch.equal(width, want_width)
     assert late > 0
+
+
+# ---- two host threads -------------------------------------------------------------------------
+
+def select_call(c, top, stream):
+    """A call of the C entry point with everything but its execution done beforehand, and its outputs."""
+    lib = qsa.load_library()
+    Tq, Hi, Di = c["q"].shape
+    B, P = c["page_table"].shape
+    block, page = c["block"], c["page_size"]
+    W = top * block + block - 1
+    idx = torch.full((Tq, W), -7, dtype=I32, device="cuda")
+    width = torch.full((Tq,), -7, dtype=I32, device="cuda")
+    need = qsa.qsa_select_slots_workspace_bytes(Tq, B, P, page, Hi, Di, block)
+    work = torch.empty(need, dtype=torch.uint8, device="cuda")
+    cu = None if c["cu_q"] is None else c["cu_q"].data_ptr()
+    args = (c["q"].data_ptr(), c["q"].stride(0), c["q"].stride(1), c["weight"].data_ptr(), c["weight"].stride(0),
+            c["codes"].data_ptr(), c["codes"].stride(0), c["scales"].data_ptr(), c["page_table"].data_ptr(), P,
+            c["seq_lens"].data_ptr(), cu, Tq, B, P, c["codes"].shape[0] * block // page, page, Hi, Di, block, top, 0, 0,
+            idx.data_ptr(), W, width.data_ptr(), work.data_ptr(), need, None, stream.cuda_stream)
+    return lambda: lib.qsa_select_slots(*args), idx, width, work
+
+
+@pytest.mark.parametrize("rows", [None, [1300]])
+def test_select_from_two_host_threads(rows):
+    """A small and a large call again and again, each in its own thread and stream: no launch of
+    one is refused for the shared memory that the other asks for."""
+    lens = [9000] if rows is None else [1900]
+    a = select_case(270, lens, rows, 64, 64, 1, 64)   # four groups of heads; thousands of blocks taken
+    b = select_case(271, [300], None if rows is None else [1300], 10, 64, 1, 64)
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    jobs = [select_call(a, 1800, streams[0]), select_call(b, 8, streams[1])]
+    torch.cuda.synchronize()
+    status = [set(), set()]
+
+    def work(i):
+        for _ in range(500):
+            status[i].add(jobs[i][0]())
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert status == [{0}, {0}]
+    for c, top, (_, idx, width, _) in ((a, 1800, jobs[0]), (b, 8, jobs[1])):
+        want, want_width = ref.select(c["q"], c["weight"], c["codes"], c["scales"], c["page_table"], c["seq_lens"],
+                                      c["cu_q"], top, 64, 1, 0, 0)
+        assert torch.equal(idx.cpu(), torch.from_numpy(want)) and torch.equal(width.cpu(), torch.from_numpy(want_width))

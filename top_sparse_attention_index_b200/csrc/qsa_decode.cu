@@ -576,8 +576,8 @@ qsa_status_t check_decode_sizes(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, i
 template <bool FP8, int NT>
 cudaError_t launch_decode(const DecodeParams& p, int blocks, cudaStream_t st) {
   using C = Decode<FP8, NT>;
-  const cudaError_t e = cudaFuncSetAttribute(qsa_paged_decode_kernel<FP8, NT>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::kSmem));
+  static std::atomic<uint64_t> done[64];
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(qsa_paged_decode_kernel<FP8, NT>), done);
   if (e != cudaSuccess) return e;
   return launch(qsa_paged_decode_kernel<FP8, NT>, blocks, C::kThreads, C::kSmem, st, p);
 }

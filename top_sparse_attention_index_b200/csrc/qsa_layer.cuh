@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -65,6 +66,27 @@ __device__ __forceinline__ uint4 load_l2(const uint4* p) {
 __device__ __forceinline__ float4 load_l2(const float4* p) {
   const uint4 x = load_l2(reinterpret_cast<const uint4*>(p));
   return make_float4(__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w));
+}
+
+// Lets a kernel have as much dynamic shared memory as the device gives a block beside the
+// kernel's own.  The limit is shared by all host threads: were it set to what one call needs, a
+// smaller call of another thread would lower it between that and the launch.  Set once in each
+// context (`done`: one per kernel, by device).
+inline cudaError_t allow_smem(const void* kernel, std::atomic<uint64_t> (&done)[64]) {
+  int dev = 0, most = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev >= 0 && dev < 64;
+  const uint64_t context = current_context_id();
+  if (known && context != 0 && done[dev].load(std::memory_order_acquire) == context) return cudaSuccess;
+  cudaFuncAttributes own{};
+  if ((e = cudaFuncGetAttributes(&own, kernel)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most - int(own.sharedSizeBytes));
+  if (e != cudaSuccess) return e;
+  const uint64_t now = current_context_id();  // (the first call made the context current)
+  if (known && now != 0) done[dev].store(now, std::memory_order_release);
+  return cudaSuccess;
 }
 
 template <class... P, class... A>

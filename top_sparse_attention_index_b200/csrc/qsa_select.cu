@@ -1385,9 +1385,10 @@ template <int DI, int HP, int NT>
 cudaError_t launch_score(SelectParams& p, int groups, int num_sms, cudaStream_t st) {
   using C = Score<DI, HP, NT>;
   const size_t smem = C::smem(groups);
-  cudaError_t e = cudaFuncSetAttribute(qsa_select_score_kernel<DI, HP, NT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-  if (e != cudaSuccess) return e;
+  // (no allow_smem: with a limit that it does not need, the kernel was left less L1, and one row
+  // over 65,535 blocks took 48 us in place of 28)
+  static_assert((HP == 16 ? QSA_MAX_INDEX_HEADS / 16 : 1) * NT * (C::kSteps * 256 + 32) <= 48 * 1024,
+                "within what every kernel may have");
   // as many blocks as the device holds, or as there are units at most
   const int rows = p.c1 - p.c0;
   const int64_t row_tiles = p.cu == nullptr ? rows : rows / C::kRows + (p.B < rows ? p.B : rows);
@@ -1424,8 +1425,8 @@ std::atomic<uint32_t> g_wait_ns{kWaitLimit};  // see qsa_probe_select_wait_ns
 
 template <int DI, int HP>
 cudaError_t launch_wide(const SelectParams& p, int chunk, int chunk_rows, int num_sms, cudaStream_t st) {
-  const cudaError_t e = cudaFuncSetAttribute(qsa_select_wide_kernel<DI, HP>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, Wide<DI>::kSmem);
+  static std::atomic<uint64_t> done[64];
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(qsa_select_wide_kernel<DI, HP>), done);
   if (e != cudaSuccess) return e;
   const int64_t max_tiles = wide_max_tiles(chunk_rows, p.B, p.Hi);
   return launch(qsa_select_wide_kernel<DI, HP>, num_sms, kWideThreads, Wide<DI>::kSmem, st, p,
@@ -1464,8 +1465,8 @@ cudaError_t launch_score_for(SelectParams& p, int num_sms, cudaStream_t st) {
 
 template <int THREADS>
 cudaError_t launch_choose_for(const SelectParams& p, size_t smem, cudaStream_t st) {
-  const cudaError_t e = cudaFuncSetAttribute(qsa_select_choose_kernel<THREADS>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  static std::atomic<uint64_t> done[64];
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(qsa_select_choose_kernel<THREADS>), done);
   if (e != cudaSuccess) return e;
   return launch(qsa_select_choose_kernel<THREADS>, p.c1 - p.c0, THREADS, smem, st, p);
 }
@@ -1477,9 +1478,7 @@ cudaError_t launch_choose(SelectParams& p, int num_sms, cudaStream_t st) {
   if (p.ld <= kPickKeys && p.top <= kPickKeys && rows > 8 * num_sms) {
     p.cap = int((p.ld + 127) / 128 * 128);
     const size_t smem = size_t(kPickWarps) * p.cap * 4;
-    const cudaError_t e = cudaFuncSetAttribute(qsa_select_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               int(smem));
-    if (e != cudaSuccess) return e;
+    static_assert(kPickWarps * (kPickKeys * 4 + sizeof(ChooseShared)) <= 48 * 1024, "within what every kernel may have");
     return launch(qsa_select_pick_kernel, (rows + kPickWarps - 1) / kPickWarps, 32 * kPickWarps, smem, st, p);
   }
   // Room for what the sample's border lets through of the longest row: the expected number and
