@@ -2,6 +2,7 @@
 calls that follow each other without a pause, scores a step apart, exact counts of slots."""
 from __future__ import annotations
 
+import math
 import threading
 
 import pytest
@@ -309,3 +310,62 @@ def test_select_from_two_host_threads(rows):
         want, want_width = ref.select(c["q"], c["weight"], c["codes"], c["scales"], c["page_table"], c["seq_lens"],
                                       c["cu_q"], top, 64, 1, 0, 0)
         assert torch.equal(idx.cpu(), torch.from_numpy(want)) and torch.equal(width.cpu(), torch.from_numpy(want_width))
+
+
+# ---- decode: every slot counts once -----------------------------------------------------------
+
+def share_borders(lens, fp8, groups):
+    """Positions (per sequence) of the first and last tokens of every thread block's share."""
+    unit = 64 if fp8 else 32  # slots that the work is shared out in
+    units = [-(-n // unit) for n in lens]
+    total = sum(units)
+    groups = min(total, groups)
+    marks = [{0, n - 1} if n else set() for n in lens]
+    for c in range(1, groups):
+        u = c * (total // groups) + min(c, total % groups)
+        for b, n in enumerate(units):
+            if u < n:
+                marks[b] |= {max(u * unit - 1, 0), u * unit}
+                break
+            u -= n
+    return marks
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens", [[100003], [30011, 12, 0, 8000, 4097, 1, 31, 33, 64, 65], [4096] * 40,
+                                  [(37 * b) % 200 for b in range(700)]], ids=["one", "ragged", "equal", "many"])
+@pytest.mark.parametrize("blocks", [0, 4, 28, 2000])
+def test_decode_counts_every_slot_once(lens, blocks, fp8):
+    """Scores of 0: every weight is 1, so the log-sum-exp is log2 of the length, and a value that
+    only one slot holds comes out divided by the length.  The marked slots are the first and last
+    ones of the thread blocks' shares, 256 per KV head.
+
+    The log-sum-exp: two approximate logarithms (2^-22 of at most 17 each) and their roundings,
+    exponentials of differences of the pieces' (2^-18): below 2^-17 + 2^-18; one slot of 100,003
+    is 2^-16.1.  The values: approximations and 32-bit sums below 2^-16, bf16 2^-8: 2^-7 in all."""
+    Hkv, page = 4, 64
+    c = decode_case(280, lens, 2 * Hkv, Hkv, page, fp8)
+    plan, _ = qsa.qsa_paged_decode_plan(len(lens), 2 * Hkv, Hkv, 256, c["page_table"].shape[1], page, fp8,
+                                        torch.cuda.get_device_properties(0).multi_processor_count, blocks)
+    marks = share_borders(lens, fp8, plan // Hkv)
+    c["v_cache"] = torch.zeros_like(c["v_cache"].float())
+    want = torch.zeros(len(lens), Hkv, 256, dtype=torch.float64, device="cuda")
+    value = 256.0
+    for b, n in enumerate(lens):
+        at = sorted(marks[b])
+        at = at[::-(-len(at) // (256 * Hkv))] if at else at
+        if not at:
+            continue
+        slots = ref.slots_of(c["page_table"][b], n, page, 10 ** 9)[torch.tensor(at, device="cuda")]
+        k = torch.arange(len(at), device="cuda")
+        c["v_cache"][slots, k // 256, k % 256] = value
+        want[b, k // 256, k % 256] = value * c.get("v_scale", 1.0) / n
+    c["v_cache"] = c["v_cache"].to(F8 if fp8 else BF)
+    lse = torch.full((len(lens), 2 * Hkv), 7.0, device="cuda")
+    out = qsa.paged_decode(**c, scale=0.0, lse=lse, blocks=blocks)
+    want = want.repeat_interleave(2, 1)
+    close(out, want, 2.0 ** -7 * want)
+    n = torch.tensor(lens, dtype=torch.float64, device="cuda")
+    want_lse = torch.log2(n)[:, None].expand_as(lse)
+    assert torch.equal(lse[n == 0], want_lse[n == 0].float())
+    assert ((lse.double() - want_lse)[n > 0].abs() <= 2.0 ** -17 + 2.0 ** -18).all()
