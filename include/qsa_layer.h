@@ -174,8 +174,12 @@ qsa_status_t qsa_select_slots(const void* q, int64_t q_stride_t, int64_t q_strid
  *                a multiple of Hkv, and smaller when there is less work); the order of the
  *                sums, and with it the last bits, depend on it.
  *   workspace    as planned, 16-byte aligned (fp32 partial outputs and log-sum-exp).
+ *   The weights are rounded to 16 bits for their product with V, in numerator and denominator
+ *   alike (bf16, 2^-8 of each; with kv_fp8 16-bit floats, 2^-11, or 2^-32 of the largest weight
+ *   where that is more); scores, sums and joins are 32-bit.
  *   D must be 256 and 1 <= Hq / Hkv <= 16.  With kv_fp8 the products run on 16-bit floats:
- *   a query element of 65536 or more sets QSA_ERRBIT_Q_RANGE (that row is not valid).
+ *   a query element of 65536 or more sets QSA_ERRBIT_Q_RANGE (that row is not valid), and one
+ *   below 2^-16 is rounded to a multiple of 2^-24.
  */
 int32_t qsa_paged_decode_plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t P,
                               int32_t page_size, int32_t kv_fp8, int32_t num_sms,

@@ -369,3 +369,34 @@ def test_decode_counts_every_slot_once(lens, blocks, fp8):
     want_lse = torch.log2(n)[:, None].expand_as(lse)
     assert torch.equal(lse[n == 0], want_lse[n == 0].float())
     assert ((lse.double() - want_lse)[n > 0].abs() <= 2.0 ** -17 + 2.0 ** -18).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("log2", [22.5, 25.5])
+def test_decode_of_dominant_tokens_keeps_the_rest(log2, fp8):
+    """262,144 tokens in one thread block; the first token of each warp outweighs every other one
+    by 2^22.5 or 2^25.5, and the output is what the others sum to (their values are 1, its is 0).
+
+    Off by, of the output: a weight 2^-8 (bf16) or 2^-25 of the largest weight's 2^7, a 16-bit
+    float's half step; the numerator's sum, 17 addends at a time cut at 2^-24 of it, over 2^13
+    steps of half its size on average: 2^-8; the store 2^-8; the denominator, by what it may
+    lose: addends below 2^-24 of a 32-bit sum, at most the others' share."""
+    n = 262144
+    c = decode_case(281, [n], 1, 1, 64, fp8, extra_pages=0)
+    warps = 4 if fp8 else 2
+    one, zero = torch.tensor([1.0, 0.0]).to(F8 if fp8 else BF)
+    c["k_scale"] = c["v_scale"] = 1.0
+    c["q"] = torch.ones_like(c["q"])
+    for name, first, others in (("k_cache", one, zero), ("v_cache", zero, one)):
+        x = c[name].view(torch.uint8)
+        x[:] = others.view(1).view(torch.uint8).cuda().repeat(256)
+        slots = ref.slots_of(c["page_table"][0], n, 64, 10 ** 9)[torch.arange(warps, device="cuda") * 16]
+        x[slots] = first.view(1).view(torch.uint8).cuda().repeat(256)
+    lse = torch.zeros(1, 1, device="cuda")
+    out = qsa.paged_decode(**c, scale=log2 * math.log(2) / 256, lse=lse, blocks=1).double()
+    rest = (n - warps) * 2.0 ** -log2
+    want, share = rest / (warps + rest), rest / warps
+    weight = 2.0 ** (log2 - 32) if fp8 else 2.0 ** -8
+    assert ((out - want).abs() <= want * (weight + 2.0 ** -8 + 2.0 ** -8 + share)).all(), (out.min(), out.max(), want)
+    # between the dominant tokens' alone and the whole sum's
+    assert math.log2(warps) - 2.0 ** -17 <= float(lse) - log2 <= math.log2(warps + rest * (1 + weight)) + 2.0 ** -17

@@ -95,6 +95,10 @@ struct Decode {
   static constexpr int kQPitch = 2 * kD + 16;
   static constexpr int kQBytes = NT * 8 * kQPitch;
   static constexpr int kMergePitch = kD + 4;
+  // What log2 of the weights is raised by: 16-bit floats have their smallest step at 2^-24, and a
+  // weight of 2^-25 of the largest or less would vanish, 262,144 of which hold 2^-7 of the sum.  The
+  // largest weight, 2^(kRescaleLog2 + 7) = 2^15, is still one of them (below 65,504).
+  static constexpr float kRaise = FP8 ? 7.f : 0.f;
   static constexpr size_t kSmem = kRing + kQBytes;
   static constexpr int kMergeBytes = kWarps * NT * 8 * kMergePitch * 4;
   // thread blocks of an SM: 228 KB of shared memory, 1 KB of each block reserved
@@ -111,8 +115,8 @@ struct Decode {
 // own: asynchronous copies into a stage while it works on the other, no block-wide barrier
 // in the loop.  Scores are S^T = K Q^T with the slots as M and the heads as N, so the group
 // shares every row that is read; the softmax is online (base 2, the reference moves only when
-// the maximum rises by more than 2^8); P is rounded to 16 bits for O^T += V^T P^T, and the
-// denominator sums the same rounded values.  The bound is HBM: every row is read once.
+// the maximum rises by more than 2^8); P is rounded to 16 bits (bf16, or f16 raised by 2^7 for
+// E4M3) for O^T += V^T P^T, and the denominator sums the same rounded values.  The bound is HBM: every row is read once.
 // 64 sequences of up to 8,192 tokens, 24 + 2 heads: 605 MB in 111 us, 0.84 of the copy rate
 // (and 8 us for the join); 4 of 262,144 tokens in E4M3: 1.07 GB in 182 us, 0.91.
 template <bool FP8, int NT>
@@ -347,7 +351,8 @@ __global__ void __launch_bounds__(Decode<FP8, NT>::kThreads) qsa_paged_decode_ke
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       // (a reference of -infinity, where no slot was valid yet: the weights are 0)
-      const float r0 = fmaxf(m_ref[n][0], -3.402823466e38f), r1 = fmaxf(m_ref[n][1], -3.402823466e38f);
+      const float r0 = fmaxf(m_ref[n][0] - C::kRaise, -3.402823466e38f);
+      const float r1 = fmaxf(m_ref[n][1] - C::kRaise, -3.402823466e38f);
       const float w0 = fast_exp2(x[n][0] - r0), w1 = fast_exp2(x[n][1] - r1);
       const float w2 = fast_exp2(x[n][2] - r0), w3 = fast_exp2(x[n][3] - r1);
       // slots g8 and g8 + 8, heads 2 t4 and 2 t4 + 1
@@ -404,7 +409,7 @@ __global__ void __launch_bounds__(Decode<FP8, NT>::kThreads) qsa_paged_decode_ke
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int g = n * 8 + 2 * t4 + c;
-      if (g8 == 0) sState[warp][g] = make_float2(m_ref[n][c], l[n][c]);
+      if (g8 == 0) sState[warp][g] = make_float2(m_ref[n][c] - C::kRaise, l[n][c]);
       float* dst = sO + (warp * NT * 8 + g) * C::kMergePitch;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
