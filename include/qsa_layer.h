@@ -158,8 +158,9 @@ qsa_status_t qsa_select_slots(const void* q, int64_t q_stride_t, int64_t q_strid
  * tokens i whose slots the page table names (slot = page_table[b, i / page_size] * page_size
  * + i mod page_size):
  *   s_i = scale * q[b, h] . k_cache[slot_i, j];   out[b, h] = sum_i softmax(s)_i v_cache[slot_i, j]
- * or exactly +0 when the sequence has no token.  The tokens of all sequences are shared out
- * evenly over the thread blocks; pieces of one sequence are joined by their log-sum-exp.
+ * or exactly +0 when the sequence has no token, and NaN (out and lse) when a score is NaN.
+ * The tokens of all sequences are shared out evenly over the thread blocks; pieces of one
+ * sequence are joined by their log-sum-exp.
  *
  *   q            bf16 [B, Hq, D], strides (b, h);  out bf16 [B, Hq, D].
  *   k_cache, v_cache   [pages * page_size, Hkv, D] (fewer than 2^31 slots, their strides

@@ -400,3 +400,30 @@ def test_decode_of_dominant_tokens_keeps_the_rest(log2, fp8):
     assert ((out - want).abs() <= want * (weight + 2.0 ** -8 + 2.0 ** -8 + share)).all(), (out.min(), out.max(), want)
     # between the dominant tokens' alone and the whole sum's
     assert math.log2(warps) - 2.0 ** -17 <= float(lse) - log2 <= math.log2(warps + rest * (1 + weight)) + 2.0 ** -17
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n", [1, 15, 16, 17, 33, 300, 5000])
+@pytest.mark.parametrize("blocks", [0, 2, 50])
+def test_decode_keeps_a_nan(n, blocks, fp8):
+    """A NaN in the last key of one KV head, or in a query, comes out in every element of the heads
+    that read it, whatever the length and the split; the others are untouched."""
+    nan = torch.tensor([0x7f], dtype=torch.uint8, device="cuda") if fp8 else \
+        torch.full((1,), float("nan"), dtype=BF, device="cuda").view(torch.uint8)
+    for what in ("key", "query", "first query"):
+        c = decode_case(282, [n, n + 3], 6, 2, 16, fp8)
+        clean_lse = torch.zeros(2, 6, device="cuda")
+        clean = qsa.paged_decode(**c, lse=clean_lse, blocks=blocks)
+        hit = torch.zeros(2, 6, dtype=torch.bool, device="cuda")
+        if what == "key":
+            slot = ref.slots_of(c["page_table"][0], n, 16, 10 ** 9)[-1]
+            c["k_cache"].view(torch.uint8)[slot, 1, :nan.numel()] = nan
+            hit[0, 3:] = True
+        else:
+            c["q"] = c["q"].clone()
+            c["q"][0, 0 if what == "first query" else 4, 77] = float("nan")
+            hit[0, 0 if what == "first query" else 4] = True
+        lse = torch.zeros(2, 6, device="cuda")
+        out = qsa.paged_decode(**c, lse=lse, blocks=blocks)
+        assert out[hit].isnan().all() and lse[hit].isnan().all()
+        assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse[~hit], clean_lse[~hit])

@@ -28,6 +28,14 @@ struct DecodeParams {
   float scale_log2, v_scale;
 };
 
+// The larger one, or a NaN if either is one: fmaxf drops it, and where every other score of a
+// piece is masked the piece then counts as empty.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float x;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(a), "f"(b));
+  return x;
+}
+
 __device__ __forceinline__ int tokens_of(const DecodeParams& p, int b, bool report) {
   const int64_t most = int64_t(p.P) * p.page_size;
   const int n = p.lens[b];
@@ -319,9 +327,9 @@ __global__ void __launch_bounds__(Decode<FP8, NT>::kThreads) qsa_paged_decode_ke
       }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        top[n][c] = fmaxf(x[n][c], x[n][c + 2]);
+        top[n][c] = max_or_nan(x[n][c], x[n][c + 2]);
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) top[n][c] = fmaxf(top[n][c], __shfl_xor_sync(0xffffffffu, top[n][c], d));
+        for (int d = 4; d < 32; d <<= 1) top[n][c] = max_or_nan(top[n][c], __shfl_xor_sync(0xffffffffu, top[n][c], d));
         rises |= top[n][c] > m_ref[n][c] + kRescaleLog2 || m_ref[n][c] == kNegInf;
       }
     }
@@ -427,7 +435,7 @@ __global__ void __launch_bounds__(Decode<FP8, NT>::kThreads) qsa_paged_decode_ke
     const int g = i / (kD / 4), d = (i % (kD / 4)) * 4;
     float top = kNegInf;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sState[w][g].x);
+    for (int w = 0; w < kWarps; ++w) top = max_or_nan(top, sState[w][g].x);
     float acc[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
@@ -488,14 +496,14 @@ __global__ void __launch_bounds__(THREADS) qsa_paged_join_kernel(const DecodePar
   const int shift = share.begin(first) < seg0 ? 1 : 0;
   auto record = [&](int i) { return (((int64_t(first) + i) * p.Hkv + j) * 2 + (i == 0 ? shift : 0)) * p.G + g; };
   float top = kNegInf;
-  for (int i = tid; i < n; i += THREADS) top = fmaxf(top, load_l2(p.ws_lse + record(i)));
+  for (int i = tid; i < n; i += THREADS) top = max_or_nan(top, load_l2(p.ws_lse + record(i)));
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  for (int d = 16; d > 0; d >>= 1) top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
   if (lane == 0) sRed[warp] = top;
   __syncthreads();
   top = sRed[0];
 #pragma unroll
-  for (int w = 1; w < THREADS / 32; ++w) top = fmaxf(top, sRed[w]);
+  for (int w = 1; w < THREADS / 32; ++w) top = max_or_nan(top, sRed[w]);
 
   const int part = tid >> 6, l = tid & 63;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
