@@ -5,6 +5,7 @@ from __future__ import annotations
 import math
 import threading
 
+import numpy as np
 import pytest
 import torch
 
@@ -427,3 +428,27 @@ def test_decode_keeps_a_nan(n, blocks, fp8):
         out = qsa.paged_decode(**c, lse=lse, blocks=blocks)
         assert out[hit].isnan().all() and lse[hit].isnan().all()
         assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse[~hit], clean_lse[~hit])
+
+
+# ---- index keys of hardly any size ------------------------------------------------------------
+
+@pytest.mark.parametrize("block", [1, 3, 8, 9, 11, 15, 16])
+def test_pack_index_keys_of_subnormal_means(block):
+    """Means of 2^-133 and little more over the block: the scale keeps few bits, a quotient can be
+    128 and more, and a code is at most 127 in magnitude, with its value's sign."""
+    n = 64
+    k = torch.arange(1, n + 1, device="cuda").double() * 2.0 ** -133  # exact bf16 subnormals (to 2^-126) and normals
+    keys = torch.zeros(n, block, 64, dtype=BF, device="cuda")
+    keys[:, 0, 0] = k.to(BF)
+    keys[:, 0, 5] = -k.to(BF)
+    keys[:, block - 1, 9] = (k / 2).to(BF)
+    codes, scales = torch.zeros(n, 64, dtype=torch.int8, device="cuda"), torch.zeros(n, device="cuda")
+    qsa.pack_index_keys(keys.view(n * block, 64), torch.arange(n, dtype=I32, device="cuda"), codes, scales, block=block)
+    x = keys.float().cpu().numpy()
+    mean = (x[:, 0] if block == 1 else x[:, 0] + x[:, block - 1]) / np.float32(block)
+    scale = np.abs(mean).max(-1) / np.float32(127)
+    want = np.clip(np.rint(mean / scale[:, None]), -127, 127)
+    assert mean.dtype == scale.dtype == np.float32 and (scale > 0).all()
+    assert torch.equal(scales.cpu(), torch.from_numpy(scale))
+    assert torch.equal(codes.cpu(), torch.from_numpy(want.astype(np.int8)))
+    assert (codes[:, 0] > 0).all() and (codes[:, 5] < 0).all()

@@ -149,13 +149,14 @@ __device__ __forceinline__ uint32_t top_bits(const float (&x)[8]) {
 // caller gets the same codes; zeros when the scale is not a positive finite number.  The
 // product with the reciprocal is within 127 * 3 * 2^-24 of the quotient (at most 127 in
 // magnitude), so it rounds to the same code unless it lies that close to a half: only then
-// are the quotients themselves taken (also when the reciprocal of a tiny scale overflows).
-// Adding 1.5 * 2^23 rounds to a whole number and leaves it in the low bits.
+// are the quotients themselves taken; also over a subnormal scale, whose reciprocal may overflow
+// and which may be so far below a 127th of the largest value that a quotient has to be held to
+// 127.  Adding 1.5 * 2^23 rounds to a whole number and leaves it in the low bits.
 __device__ __forceinline__ uint2 int8x8_codes(const float (&x)[8], float scale) {
   if (!(scale > 0.f && scale < __builtin_huge_valf())) return make_uint2(0u, 0u);
   const float inv = __frcp_rn(scale);
   uint32_t c[8];
-  bool close = false;
+  bool close = scale < 0x1p-126f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float q = __fmul_rn(x[i], inv), t = __fadd_rn(q, 12582912.f);
@@ -168,7 +169,8 @@ __device__ __forceinline__ uint2 int8x8_codes(const float (&x)[8], float scale) 
       float v = x[0];  // x[i], without an index into registers
 #pragma unroll
       for (int k = 1; k < 8; ++k) v = i == k ? x[k] : v;
-      const uint32_t q = __float_as_uint(__fadd_rn(__fdiv_rn(v, scale), 12582912.f));
+      const float ratio = fminf(fmaxf(__fdiv_rn(v, scale), -127.f), 127.f);
+      const uint32_t q = __float_as_uint(__fadd_rn(ratio, 12582912.f));
 #pragma unroll
       for (int k = 0; k < 8; ++k) c[k] = i == k ? q : c[k];
     }
