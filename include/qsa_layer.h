@@ -64,7 +64,8 @@ extern "C" {
  *                 bf16, or with kv_fp8 E4M3 codes of x * (1 / k_scale) (x * (1 / v_scale)),
  *                 saturated (strides in bytes).  slots[t] = -1 stores nothing; another value outside
  *                 [0, rows) stores nothing and sets QSA_ERRBIT_SLOT_RANGE.  When two tokens
- *                 name one slot, what it holds is unspecified.
+ *                 name one slot, what it holds is unspecified.  With slots and rows = 0 the
+ *                 destinations may be NULL.
  *   D is 64, 128 or 256; rot is a multiple of 16, at most D (0: no rotation).
  * Pointers are 16-byte aligned (positions, inv_freq, slots: 4) and strides multiples of 16
  * bytes (8 bytes for E4M3 destinations).

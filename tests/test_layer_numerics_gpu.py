@@ -12,7 +12,7 @@ import torch
 import layer_reference as ref
 import top_sparse_attention_index_b200 as qsa
 from test_layer_gpu import (BF, F8, I32, check_select, close, decode_case, err_word, gen, keyed_case, normal,
-                            run_select, select_case)
+                            rope_case, run_select, select_case)
 
 pytestmark = pytest.mark.gpu
 
@@ -452,3 +452,18 @@ def test_pack_index_keys_of_subnormal_means(block):
     assert torch.equal(scales.cpu(), torch.from_numpy(scale))
     assert torch.equal(codes.cpu(), torch.from_numpy(want.astype(np.int8)))
     assert (codes[:, 0] > 0).all() and (codes[:, 5] < 0).all()
+
+
+# ---- a cache without a slot -------------------------------------------------------------------
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_norm_rope_into_an_empty_pool(fp8):
+    """No token has a slot: queries are turned as ever, nothing is stored, a slot is reported."""
+    c = rope_case(290, 5, 4, 2, 128, 64, 1)
+    want, _ = qsa.qk_norm_rope(c["q"], c["positions"], c["inv_freq"])
+    pool = torch.zeros(0, 2, 128, dtype=F8 if fp8 else BF, device="cuda")
+    for slot, bits in ((-1, 0), (0, qsa.QSA_ERRBIT_SLOT_RANGE)):
+        err = err_word()
+        got, keys = qsa.qk_norm_rope(c["q"], c["positions"], c["inv_freq"], k=c["k"], v=c["v"], k_cache=pool,
+                                     v_cache=pool, slots=torch.full((5,), slot, dtype=I32, device="cuda"), err_word=err)
+        assert torch.equal(got, want) and keys is None and int(err) == bits

@@ -345,8 +345,10 @@ extern "C" qsa_status_t qsa_qk_norm_rope(
   }
   if (T == 0 || (Hq == 0 && Hkv == 0)) return QSA_OK;
   if (Hq > 0 && (q == nullptr || q_out == nullptr)) QSA_REJECT(QSA_ERR_INVALID_ARG, "NULL q or q_out");
-  if (Hkv > 0 && (k == nullptr || k_dst == nullptr)) QSA_REJECT(QSA_ERR_INVALID_ARG, "NULL k or k_dst");
-  if ((v == nullptr) != (v_dst == nullptr) || (v != nullptr && Hkv == 0))
+  const bool no_pool = rows == 0 && slots != nullptr;  // of no row: every token is dropped, the pool may be NULL
+  if (Hkv > 0 && (k == nullptr || (k_dst == nullptr && !no_pool)))
+    QSA_REJECT(QSA_ERR_INVALID_ARG, "NULL k or k_dst");
+  if (((v == nullptr) != (v_dst == nullptr) && !no_pool) || (v != nullptr && Hkv == 0))
     QSA_REJECT(QSA_ERR_INVALID_ARG, "v and v_dst must come together, with k");
   if (rot > 0 && (positions == nullptr || inv_freq == nullptr))
     QSA_REJECT(QSA_ERR_INVALID_ARG, "NULL positions or inv_freq with rot=%d", rot);
