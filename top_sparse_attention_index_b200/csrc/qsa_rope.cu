@@ -393,14 +393,20 @@ extern "C" qsa_status_t qsa_qk_norm_rope(
   p.T = T, p.Hq = Hq, p.Hkv = Hkv, p.interleaved = interleaved;
   p.offset = weight_offset, p.eps = eps, p.rope_scale = rope_scale;
   p.inv_k_scale = 1.0f / k_scale, p.inv_v_scale = 1.0f / v_scale, p.kv_fp8 = kv_fp8;
-  // A warp takes a whole token once that gives every SM some 32 warps, else as many steps as
-  // do, at least two (it makes its token's sines and cosines, about the work of three steps).
+  int dev = 0, num_sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return launch_status(e, "qsa_qk_norm_rope");
+  // A warp takes a whole token once that makes 32 warps for every SM (of which 20 run at a time),
+  // else as many steps as do, at least two (it makes its token's sines and cosines, about the
+  // work of three steps).
   const int per_step = 512 / D;
   p.q_steps = (Hq + per_step - 1) / per_step;
   p.k_steps = k != nullptr ? (Hkv + per_step - 1) / per_step : 0;
   p.v_steps = v != nullptr ? (Hkv + per_step - 1) / per_step : 0;
   const int64_t all = p.q_steps + p.k_steps + p.v_steps;
-  int64_t steps = (int64_t(T) * all + 148 * 32 - 1) / (148 * 32);
+  const int64_t warps = int64_t(num_sms) * 32;
+  int64_t steps = (int64_t(T) * all + warps - 1) / warps;
   steps = steps < 2 ? 2 : steps;
   p.parts = int32_t((all + steps - 1) / steps);
   p.steps = int32_t((all + p.parts - 1) / p.parts);
