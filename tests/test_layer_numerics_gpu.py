@@ -467,3 +467,51 @@ def test_norm_rope_into_an_empty_pool(fp8):
         got, keys = qsa.qk_norm_rope(c["q"], c["positions"], c["inv_freq"], k=c["k"], v=c["v"], k_cache=pool,
                                      v_cache=pool, slots=torch.full((5,), slot, dtype=I32, device="cuda"), err_word=err)
         assert torch.equal(got, want) and keys is None and int(err) == bits
+
+
+# ---- different calls at once, and one workspace of several graphs -----------------------------
+
+def test_different_calls_at_once():
+    """Two streams, each with selections and decodes of its own in turn."""
+    jobs = [(select_state(300 + i, [9000 - 64 * i, 3000], [300, 200 + i]), decode_case(310 + i, [9000, 40 + i], 16, 2, 64,
+                                                                                     i % 2 == 1)) for i in range(4)]
+    want = []
+    for s, d in jobs:
+        want.append((*qsa.select_slots(**s, top_blocks=100), qsa.paged_decode(**d)))
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for turn in range(12):
+        for i, stream in enumerate(streams):
+            n = 2 * i + turn % 2
+            s, d = jobs[n]
+            got.append((n, (*qsa.select_slots(**s, top_blocks=100, stream=stream), qsa.paged_decode(**d, stream=stream))))
+    torch.cuda.synchronize()
+    for n, outs in got:
+        assert all(torch.equal(a, b) for a, b in zip(outs, want[n]))
+
+
+def test_graphs_that_share_a_workspace():
+    """Captured calls of different inputs over one workspace, replayed in turn without a pause."""
+    states = [select_state(320 + i, [9000 - 64 * i, 3000], [300, 200]) for i in range(3)]
+    caches = [decode_case(330 + i, [9000 - i, 40], 16, 2, 64) for i in range(3)]
+    sizes = [qsa.qsa_select_slots_workspace_bytes(500, 2, 141, 64, 4, 128, 4),
+             qsa.qsa_paged_decode_plan(2, 16, 2, 256, 142, 64, False, 148, 0)[1]]
+    work = torch.empty(max(sizes) * 2, dtype=torch.uint8, device="cuda")
+    want, outs, graphs = [], [], []
+    for s, d in zip(states, caches):
+        want.append((*qsa.select_slots(**s, top_blocks=100), qsa.paged_decode(**d)))
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append((*qsa.select_slots(**s, top_blocks=100, workspace=work), qsa.paged_decode(**d, workspace=work)))
+        graphs.append(graph)
+    for _ in range(8):
+        for out in outs:
+            for x in out:
+                x.fill_(-5)
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for out, exp in zip(outs, want):
+            assert all(torch.equal(a, b) for a, b in zip(out, exp))
