@@ -182,7 +182,7 @@ qsa_status_t qsa_select_slots(const void* q, int64_t q_stride_t, int64_t q_strid
  *   where that is more); scores, sums and joins are 32-bit.
  *   D must be 256 and 1 <= Hq / Hkv <= 16.  With kv_fp8 the products run on 16-bit floats:
  *   a query element of 65536 or more sets QSA_ERRBIT_Q_RANGE (that row is not valid), and one
- *   below 2^-16 is rounded to a multiple of 2^-24.
+ *   below 2^-17 is rounded to a multiple of 2^-24.
  */
 int32_t qsa_paged_decode_plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t P,
                               int32_t page_size, int32_t kv_fp8, int32_t num_sms,

@@ -256,7 +256,8 @@ __global__ void __launch_bounds__(Decode<FP8, NT>::kThreads) qsa_paged_decode_ke
 
   float o[NT][16][4];  // O^T: 16 m-tiles of 16 dimensions
   float l[NT][4];      // P's sums over the slots: an m-tile whose A is all ones
-  float m_ref[NT][2];
+  float m_ref[NT][2];  // a maximum less kRaise; moves when one is more than kMove above it
+  constexpr float kMove = kRescaleLog2 + C::kRaise;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     m_ref[n][0] = m_ref[n][1] = kNegInf;
@@ -330,7 +331,7 @@ __global__ void __launch_bounds__(Decode<FP8, NT>::kThreads) qsa_paged_decode_ke
         top[n][c] = max_or_nan(x[n][c], x[n][c + 2]);
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) top[n][c] = max_or_nan(top[n][c], __shfl_xor_sync(0xffffffffu, top[n][c], d));
-        rises |= top[n][c] > m_ref[n][c] + kRescaleLog2 || m_ref[n][c] == kNegInf;
+        rises |= top[n][c] > m_ref[n][c] + kMove || m_ref[n][c] == kNegInf;
       }
     }
     if (__any_sync(0xffffffffu, rises)) {  // some head's reference moves
@@ -338,9 +339,10 @@ __global__ void __launch_bounds__(Decode<FP8, NT>::kThreads) qsa_paged_decode_ke
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          if (!(top[n][c] > m_ref[n][c] + kRescaleLog2 || m_ref[n][c] == kNegInf)) continue;
+          if (!(top[n][c] > m_ref[n][c] + kMove || m_ref[n][c] == kNegInf)) continue;
+          const float m_new = top[n][c] - C::kRaise;
           if (m_ref[n][c] != kNegInf) {
-            const float f = fast_exp2(m_ref[n][c] - top[n][c]);
+            const float f = fast_exp2(m_ref[n][c] - m_new);
             l[n][c] *= f;
             l[n][c + 2] *= f;
 #pragma unroll
@@ -349,7 +351,7 @@ __global__ void __launch_bounds__(Decode<FP8, NT>::kThreads) qsa_paged_decode_ke
               o[n][i][c + 2] *= f;
             }
           }
-          m_ref[n][c] = top[n][c];
+          m_ref[n][c] = m_new;
         }
       }
     }
@@ -359,8 +361,7 @@ __global__ void __launch_bounds__(Decode<FP8, NT>::kThreads) qsa_paged_decode_ke
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       // (a reference of -infinity, where no slot was valid yet: the weights are 0)
-      const float r0 = fmaxf(m_ref[n][0] - C::kRaise, -3.402823466e38f);
-      const float r1 = fmaxf(m_ref[n][1] - C::kRaise, -3.402823466e38f);
+      const float r0 = fmaxf(m_ref[n][0], -3.402823466e38f), r1 = fmaxf(m_ref[n][1], -3.402823466e38f);
       const float w0 = fast_exp2(x[n][0] - r0), w1 = fast_exp2(x[n][1] - r1);
       const float w2 = fast_exp2(x[n][2] - r0), w3 = fast_exp2(x[n][3] - r1);
       // slots g8 and g8 + 8, heads 2 t4 and 2 t4 + 1
@@ -417,7 +418,7 @@ __global__ void __launch_bounds__(Decode<FP8, NT>::kThreads) qsa_paged_decode_ke
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int g = n * 8 + 2 * t4 + c;
-      if (g8 == 0) sState[warp][g] = make_float2(m_ref[n][c] - C::kRaise, l[n][c]);
+      if (g8 == 0) sState[warp][g] = make_float2(m_ref[n][c], l[n][c]);
       float* dst = sO + (warp * NT * 8 + g) * C::kMergePitch;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
