@@ -139,7 +139,11 @@ qsa_status_t qsa_pack_index_keys(const void* keys, int64_t key_stride_s, const i
  *               QSA_ERRBIT_WIDTH_RANGE, and the rows are not valid: slots of the pool, or -1.
  *   1 <= Hi <= 64, Di 64 or 128, block 1..16, top_blocks >= 1 with top_blocks * block <= 8192,
  *   sink_blocks + local_blocks <= top_blocks.
- *   workspace   qsa_select_slots_workspace_bytes(...) bytes, 256-byte aligned.
+ *   workspace   qsa_select_slots_workspace_bytes(...) bytes, 256-byte aligned.  They hold the
+ *               32-bit scores of a chunk of rows (512 MiB, or 64 rows where those are more)
+ *               and, with many rows per sequence and at most 32 heads, the codes of all
+ *               query rows: about Tq H (Di + 4) bytes, H the heads rounded up to a power of
+ *               two, and 256 (Di + 4) more for each sequence of each chunk.
  */
 size_t qsa_select_slots_workspace_bytes(int32_t Tq, int32_t B, int32_t P, int32_t page_size,
                                         int32_t Hi, int32_t Di, int32_t block);

@@ -17,7 +17,7 @@ using namespace qsa;
 constexpr int kKeyTile = 128;                 // micro-blocks per tile
 constexpr int kScoreThreads = 256;
 constexpr int kScoreBlocks = 2;               // of an SM
-constexpr int64_t kChunkBytes = 512 << 20;    // most scores of one chunk of rows
+constexpr int64_t kChunkBytes = 512 << 20;    // scores of one chunk of rows, while that is kMinChunkRows
 constexpr int kMinChunkRows = 64;
 constexpr int32_t kLate = 1 << 30;            // of a tile's number of rows (at most 256): see SelectParams
 
@@ -488,7 +488,7 @@ struct Wide {
 // instructions, not the MMAs (512 cycles of a unit's 3,400): per pair of dots an
 // add-with-maximum each (the integer to float conversion 2^23 + max(d, 0) and the clamp at
 // once; a dot of 128 codes is below 2^21), and a packed subtraction, product and sum.
-// 7,810 rows of 4 heads over 14,400 to 16,384 blocks of 128 codes: 181 us, 0.68 P op/s (the
+// 7,810 rows of 4 heads over 14,400 to 16,384 blocks of 128 codes: 186 us, 0.66 P op/s (the
 // same through warp-level MMAs with 64 columns a thread block took 1,000 us); eight warps
 // with 128 columns each were 7 % slower, and neither the stores, the gains' loads nor the
 // conversion's form (int to float instructions, or the subtraction folded into the product)
@@ -1113,8 +1113,10 @@ __global__ void __launch_bounds__(32 * kPickWarps) qsa_select_pick_kernel(const 
 
 // One thread block per row.  A row of at most `cap` blocks has its keys in shared memory.  Of
 // a longer one, the keys above a border estimated from kSample of them are collected there
-// in one pass (the estimate leaves out too much, or not enough, for about one row in 10^6,
-// and for keys that repeat with the sample's period: such a row searches its keys in place).
+// in one pass.  For about one row in 400 of random scores that is more than there is room for,
+// and the row is collected again above a better border; one that still does not fit, or an
+// estimate that left out too many (keys that repeat with the sample's period), has its keys
+// searched in place.
 // The exact border follows from what was collected; a bit per block marks the taken ones,
 // and a scan over the marks gives them their places in ascending order.
 // Bound: instructions and the latency of its steps, 10 rows to an SM; the scores are read
@@ -1407,6 +1409,8 @@ int heads_padded(int Hi) {
 // columns are filled to more than a half on average.  16 sequences of 16,384 tokens, whole
 // calls, the few-rows form against this one: 4 heads, 16 rows each 35 against 40 us, 32 rows
 // 48 / 51, 64 rows 62 / 51, 128 rows 101 / 70; 16 heads, 8 rows 33 / 38, 16 rows 39 / 36.
+// The average decides for all of a call's sequences, so the single rows among many long ones
+// take a tile each; 33 to 64 heads always take the few-rows form.
 bool use_wide(int32_t Tq, int32_t B, int32_t Hi, bool has_cu) {
   return has_cu && Hi <= 32 && int64_t(Tq) * heads_padded(Hi) * 2 > int64_t(B) * kWideCols;
 }

@@ -55,8 +55,8 @@ def qk_norm_rope(q, positions, inv_freq, k=None, v=None, q_weight=None, k_weight
     [T], or [axes, T] with ``sections``: how many of the rotated pairs each axis turns;
     inv_freq float32 [rot / 2].  Pairs are (i, i + rot / 2), or (2 i, 2 i + 1) with
     ``interleaved``.  Row t of k and v goes to row slots[t] (int32, -1 = not stored) of
-    k_cache / v_cache [S, Hkv, D], bf16 or float8_e4m3fn (then divided by k_scale / v_scale
-    and saturated).  Without k_cache the rotated keys come back as a new tensor.  q_out may
+    k_cache / v_cache [S, Hkv, D], bf16 or float8_e4m3fn (then multiplied by 1 / k_scale or
+    1 / v_scale, a 32-bit number, and saturated).  Without k_cache the rotated keys come back as a new tensor.  q_out may
     be q.  Returns (q_out, rotated keys or None).
     """
     return _call("qk_norm_rope", stream, q, positions, inv_freq, k, v, q_weight, k_weight, eps, weight_offset,
