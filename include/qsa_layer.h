@@ -90,7 +90,7 @@ qsa_status_t qsa_qk_norm_rope(const void* q, int64_t q_stride_t, int64_t q_strid
  * For every i < n with b = blocks[i] >= 0:
  *   m = (keys[b block] + ... + keys[b block + block - 1]) / block     (32-bit, in slot order)
  *   scales[b] = max |m| / 127,   codes[b] = round-half-even(m / scales[b])   (0 when the scale is 0;
- *   at most 127 in magnitude, which a subnormal scale, itself rounded, may exceed)
+ *   held to 127 in magnitude, which a quotient over a subnormal scale, itself rounded, may exceed)
  * A block whose keys hold a non-finite value gets codes 0 and a NaN scale, which the
  * selection ranks last.
  *
